@@ -23,11 +23,16 @@ from ._lib import (  # noqa: F401  (re-exported C ABI names)
     jfa_onebit_attend, jfa_onebit_pack, jfa_onebit_pool_bytes,
     jfa_fp4_scores, jfa_pack_kv, jfa_sparse_attend, jfa_topk, jfa_topk_blocks,
     jfa_unpack_record, jfa_workspace_layout_get, load)
+from .paged import (PagedKVCache, PagedWorkspace, PageTable, RotaryPlan, paged_append,
+                    paged_attend, paged_decode_step, paged_fork, paged_gather, paged_move,
+                    qk_norm_rope)
 
 __all__ = ["KVCache", "Workspace", "decode_step", "decode_step_blocks", "decode_step_ragged",
            "append_decode_step", "FP4KeyPool", "fp4_decode_step", "sparse_attend",
            "ChannelKeys", "channel_decode_step", "OneBitCache", "onebit_attend", "DecodeGraph",
-           "JfaError", "load"]
+           "RotaryPlan", "qk_norm_rope", "PageTable", "PagedKVCache", "PagedWorkspace",
+           "paged_append", "paged_gather", "paged_attend", "paged_fork", "paged_move",
+           "paged_decode_step", "JfaError", "load"]
 
 
 def _torch():

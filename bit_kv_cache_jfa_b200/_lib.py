@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int32, c_size_t, c_uint8, c_uint16, c_uint32, c_void_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_uint8, c_uint16, c_uint32, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libjfa.so")
 
@@ -26,10 +26,12 @@ KEY_GROUP = 64
 VAL_GROUP = 32
 TAIL_MAX = 64
 MAX_GQA = 8
+MAX_BATCH = 256
 MAX_TOPK = 4096
 MAX_EXACT = 8192
 BLOCK_TOKENS = 128
 MAX_BLOCKS = MAX_EXACT // BLOCK_TOKENS
+PAGE_RECORD_BYTES = 9728
 
 
 class JfaError(RuntimeError):
@@ -64,6 +66,24 @@ class WorkspaceLayout(ctypes.Structure):
                 ("off_bkeys", c_size_t), ("off_chan", c_size_t), ("off_qstage", c_size_t),
                 ("max_topk", c_int32), ("partial_slots", c_int32), ("cand_cap", c_int32),
                 ("reserved", c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("n_tokens", c_int32), ("num_heads", c_int32), ("num_kv_heads", c_int32),
+                ("rotary_dim", c_int32), ("interleaved", c_int32), ("positions64", c_int32),
+                ("eps", c_float), ("amplitude", c_float),
+                ("q", c_void_p), ("k", c_void_p), ("q_out", c_void_p), ("k_out", c_void_p),
+                ("q_tok", c_int64), ("q_head", c_int64), ("k_tok", c_int64), ("k_head", c_int64),
+                ("qo_tok", c_int64), ("qo_head", c_int64), ("ko_tok", c_int64), ("ko_head", c_int64),
+                ("q_weight", c_void_p), ("k_weight", c_void_p),
+                ("positions", c_void_p), ("freq", c_void_p)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("batch", c_int32), ("num_heads", c_int32), ("num_kv_heads", c_int32),
+                ("n_pages", c_int32), ("max_pages", c_int32), ("reserved", c_int32),
+                ("pages", c_void_p), ("tail_k", c_void_p), ("tail_v", c_void_p),
+                ("table", c_void_p), ("seq_lens", c_void_p)]
 
 
 # name -> (restype, argtypes) for every symbol include/jfa.h declares
@@ -123,6 +143,18 @@ SIGNATURES = {
     "jfa_channel_decode_step": (c_int32, [POINTER(Geom), c_void_p, c_void_p, c_void_p, c_float,
                                           c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
                                           c_void_p, c_void_p, c_void_p]),
+    "jfa_qk_norm_rope": (c_int32, [POINTER(Rope), c_void_p]),
+    "jfa_paged_workspace_bytes": (c_int32, [POINTER(Paged), POINTER(c_size_t)]),
+    "jfa_paged_append": (c_int32, [POINTER(Paged), c_void_p, c_int64, c_int64, c_void_p, c_int64,
+                                   c_int64, c_void_p, c_int32, c_void_p, c_void_p]),
+    "jfa_paged_gather": (c_int32, [POINTER(Paged), c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
+                                   c_void_p, c_void_p]),
+    "jfa_paged_attend": (c_int32, [POINTER(Paged), c_void_p, c_int64, c_float, c_int32, c_int32,
+                                   c_void_p, c_void_p, c_void_p, c_void_p]),
+    "jfa_paged_fork": (c_int32, [POINTER(Paged), c_void_p, c_int32, c_void_p, c_void_p]),
+    "jfa_paged_move": (c_int32, [POINTER(Paged), c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),
+    "jfa_paged_check_error": (c_int32, [POINTER(Paged), c_void_p, c_void_p, POINTER(c_uint32)]),
+    "jfa_paged_clear_error": (c_int32, [POINTER(Paged), c_void_p, c_void_p]),
 }
 
 _lib = None
@@ -293,6 +325,53 @@ def jfa_channel_decode_step(geom, k_t, k_max, q, scale, r, k, idx, k_exact, v_ex
                                           scale, r, k, _ptr(idx), _ptr(k_exact), _ptr(v_exact),
                                           int(exact_on_host), _ptr(ws), _ptr(out),
                                           _stream(stream))
+
+
+def jfa_qk_norm_rope(rope, stream=None) -> int:
+    return load().jfa_qk_norm_rope(ctypes.byref(rope), _stream(stream))
+
+
+def jfa_paged_workspace_bytes(cache) -> int:
+    n = c_size_t(0)
+    check(load().jfa_paged_workspace_bytes(ctypes.byref(cache), ctypes.byref(n)),
+          "jfa_paged_workspace_bytes")
+    return n.value
+
+
+def jfa_paged_append(cache, k_new, k_tok, k_head, v_new, v_tok, v_head, cu, n_total, ws,
+                     stream=None) -> int:
+    return load().jfa_paged_append(ctypes.byref(cache), _ptr(k_new), k_tok, k_head, _ptr(v_new),
+                                   v_tok, v_head, _ptr(cu), n_total, _ptr(ws), _stream(stream))
+
+
+def jfa_paged_gather(cache, cu, start, n_total, k_out, v_out, ws, stream=None) -> int:
+    return load().jfa_paged_gather(ctypes.byref(cache), _ptr(cu), _ptr(start), n_total,
+                                   _ptr(k_out), _ptr(v_out), _ptr(ws), _stream(stream))
+
+
+def jfa_paged_attend(cache, q, q_row, scale, window, sinks, ws, out, lse=None, stream=None) -> int:
+    return load().jfa_paged_attend(ctypes.byref(cache), _ptr(q), q_row, scale, window, sinks,
+                                   _ptr(ws), _ptr(out), _ptr(lse), _stream(stream))
+
+
+def jfa_paged_fork(cache, pairs, n, ws, stream=None) -> int:
+    return load().jfa_paged_fork(ctypes.byref(cache), _ptr(pairs), n, _ptr(ws), _stream(stream))
+
+
+def jfa_paged_move(cache, moves, n, remap, ws, stream=None) -> int:
+    return load().jfa_paged_move(ctypes.byref(cache), _ptr(moves), n, _ptr(remap), _ptr(ws),
+                                 _stream(stream))
+
+
+def jfa_paged_check_error(cache, ws, stream=None) -> tuple[int, int]:
+    flag = c_uint32(0)
+    st = load().jfa_paged_check_error(ctypes.byref(cache), _ptr(ws), _stream(stream),
+                                      ctypes.byref(flag))
+    return st, flag.value
+
+
+def jfa_paged_clear_error(cache, ws, stream=None) -> int:
+    return load().jfa_paged_clear_error(ctypes.byref(cache), _ptr(ws), _stream(stream))
 
 
 def _lens(seq_lens):

@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include "jfa_fp4.cuh"
+#include "jfa_paged.cuh"
 
 namespace jfa {
 
@@ -386,6 +387,135 @@ int jfa_onebit_attend(const jfa_geom* geom, const void* pool, const uint16_t* q,
   workspace_layout(*geom, 1, &L);
   return launch_onebit_attend(*geom, static_cast<const uint8_t*>(pool), q, scale, k_exact, v_exact,
                               static_cast<uint8_t*>(ws), L, out, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// head norms and rotary positions; the paged 4-bit cache
+// ---------------------------------------------------------------------------
+static bool row8(int64_t stride) { return stride % 8 == 0; }  // 16-byte chunks of bf16 rows
+
+int jfa_qk_norm_rope(const jfa_rope* r, void* stream) {
+  if (!r || r->n_tokens < 0 || r->num_heads < 0 || r->num_kv_heads < 0) return JFA_ERR_INVALID_ARG;
+  if (r->num_heads > (1 << 20) || r->num_kv_heads > (1 << 20)) return JFA_ERR_UNSUPPORTED;
+  if (r->rotary_dim < 2 || r->rotary_dim > kD || r->rotary_dim % 2) return JFA_ERR_INVALID_ARG;
+  if (!(r->eps >= 0.f) || r->amplitude != r->amplitude) return JFA_ERR_INVALID_ARG;
+  if (r->n_tokens == 0 || r->num_heads + r->num_kv_heads == 0) return JFA_OK;
+  if (!r->positions || !aligned(r->positions, r->positions64 ? 8 : 4) || !r->freq || !aligned(r->freq, 8))
+    return JFA_ERR_INVALID_ARG;
+  if (r->num_heads && (!r->q || !r->q_out || !aligned(r->q, 16) || !aligned(r->q_out, 16) || !row8(r->q_tok) ||
+                       !row8(r->q_head) || !row8(r->qo_tok) || !row8(r->qo_head)))
+    return JFA_ERR_INVALID_ARG;
+  if (r->num_kv_heads && (!r->k || !r->k_out || !aligned(r->k, 16) || !aligned(r->k_out, 16) ||
+                          !row8(r->k_tok) || !row8(r->k_head) || !row8(r->ko_tok) || !row8(r->ko_head)))
+    return JFA_ERR_INVALID_ARG;
+  if (!aligned(r->q_weight, 16) || !aligned(r->k_weight, 16)) return JFA_ERR_INVALID_ARG;
+  return launch_qk_norm_rope(*r, static_cast<cudaStream_t>(stream));
+}
+
+// Sizes of a paged cache.  Kernels count items (groups and tail items of
+// every sequence and KV head) in 32 bits.
+static int paged_geom(const jfa_paged* c) {
+  if (!c || c->batch < 1 || c->batch > kMaxBatch || c->num_heads < 1 || c->num_kv_heads < 1)
+    return JFA_ERR_INVALID_ARG;
+  if (c->num_heads % c->num_kv_heads != 0 || c->num_heads / c->num_kv_heads > kMaxG) return JFA_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->max_pages < 1) return JFA_ERR_INVALID_ARG;
+  if (c->num_kv_heads > 65535 || c->max_pages > (0x7FFFFFFF - kTail) / kKG) return JFA_ERR_UNSUPPORTED;
+  if ((long long)c->num_kv_heads * c->batch * ((long long)c->max_pages + kTail / 16 + 1) > 0x7FFFFFFFll)
+    return JFA_ERR_UNSUPPORTED;
+  return JFA_OK;
+}
+
+static int paged_args(const jfa_paged* c, const void* ws) {
+  const int s = paged_geom(c);
+  if (s != JFA_OK) return s;
+  if (!c->pages || !c->tail_k || !c->tail_v || !c->table || !c->seq_lens || !ws) return JFA_ERR_INVALID_ARG;
+  if (!aligned(c->pages, 16) || !aligned(c->tail_k, 16) || !aligned(c->tail_v, 16) || !aligned(c->table, 4) ||
+      !aligned(c->seq_lens, 4) || !aligned(ws, 256))
+    return JFA_ERR_INVALID_ARG;
+  return JFA_OK;
+}
+
+int jfa_paged_workspace_bytes(const jfa_paged* cache, size_t* bytes) {
+  const int s = paged_geom(cache);
+  if (s != JFA_OK) return s;
+  if (!bytes) return JFA_ERR_INVALID_ARG;
+  *bytes = paged_ws(cache->batch, cache->num_kv_heads).total;
+  return JFA_OK;
+}
+
+int jfa_paged_append(const jfa_paged* cache, const uint16_t* k_new, int64_t k_tok, int64_t k_head,
+                     const uint16_t* v_new, int64_t v_tok, int64_t v_head, const int32_t* cu,
+                     int32_t n_total, void* ws, void* stream) {
+  const int s = paged_args(cache, ws);
+  if (s != JFA_OK) return s;
+  if (n_total < 0 || (!cu && n_total % cache->batch != 0) || !aligned(cu, 4)) return JFA_ERR_INVALID_ARG;
+  if (n_total == 0) return JFA_OK;
+  if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16) || !row8(k_tok) || !row8(k_head) ||
+      !row8(v_tok) || !row8(v_head))
+    return JFA_ERR_INVALID_ARG;
+  return launch_paged_append(*cache, k_new, k_tok, k_head, v_new, v_tok, v_head, cu, n_total,
+                             static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
+}
+
+int jfa_paged_gather(const jfa_paged* cache, const int32_t* cu, const int32_t* start,
+                     int32_t n_total, uint16_t* k_out, uint16_t* v_out, void* ws, void* stream) {
+  const int s = paged_args(cache, ws);
+  if (s != JFA_OK) return s;
+  if (n_total < 0 || !cu || !aligned(cu, 4) || !aligned(start, 4)) return JFA_ERR_INVALID_ARG;
+  if (n_total == 0) return JFA_OK;
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return JFA_ERR_INVALID_ARG;
+  return launch_paged_gather(*cache, cu, start, n_total, k_out, v_out, static_cast<uint8_t*>(ws),
+                             static_cast<cudaStream_t>(stream));
+}
+
+int jfa_paged_attend(const jfa_paged* cache, const uint16_t* q, int64_t q_row, float scale,
+                     int32_t window, int32_t sinks, void* ws, uint16_t* out, float* lse,
+                     void* stream) {
+  const int s = paged_args(cache, ws);
+  if (s != JFA_OK) return s;
+  if (!q || !aligned(q, 16) || !row8(q_row) || !(scale > 0.f) || window < 0 || sinks < 0 || !out ||
+      !aligned(out, 16) || !aligned(lse, 4))
+    return JFA_ERR_INVALID_ARG;
+  return launch_paged_attend(*cache, q, q_row, scale, window, sinks, static_cast<uint8_t*>(ws), out, lse,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int jfa_paged_fork(const jfa_paged* cache, const int32_t* pairs, int32_t n, void* ws, void* stream) {
+  const int s = paged_args(cache, ws);
+  if (s != JFA_OK) return s;
+  if (n < 0 || n > cache->batch) return JFA_ERR_INVALID_ARG;
+  if (n == 0) return JFA_OK;
+  if (!pairs || !aligned(pairs, 4)) return JFA_ERR_INVALID_ARG;
+  return launch_paged_fork(*cache, pairs, n, static_cast<uint8_t*>(ws), static_cast<cudaStream_t>(stream));
+}
+
+int jfa_paged_move(const jfa_paged* cache, const int32_t* moves, int32_t n, const int32_t* remap,
+                   void* ws, void* stream) {
+  const int s = paged_args(cache, ws);
+  if (s != JFA_OK) return s;
+  if (n < 0 || n > cache->n_pages || (n > 0 && !moves) || !aligned(moves, 4) || !aligned(remap, 4))
+    return JFA_ERR_INVALID_ARG;
+  return launch_paged_move(*cache, moves, n, remap, static_cast<uint8_t*>(ws),
+                           static_cast<cudaStream_t>(stream));
+}
+
+int jfa_paged_clear_error(const jfa_paged* cache, void* ws, void* stream) {
+  if (paged_geom(cache) != JFA_OK || !ws) return JFA_ERR_INVALID_ARG;
+  uint8_t* flag = static_cast<uint8_t*>(ws) + paged_ws(cache->batch, cache->num_kv_heads).off_flag;
+  return cudaMemsetAsync(flag, 0, sizeof(uint32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? JFA_OK
+             : JFA_ERR_CUDA;
+}
+
+int jfa_paged_check_error(const jfa_paged* cache, void* ws, void* stream, uint32_t* flag_out) {
+  if (paged_geom(cache) != JFA_OK || !ws) return JFA_ERR_INVALID_ARG;
+  const uint8_t* flag = static_cast<const uint8_t*>(ws) + paged_ws(cache->batch, cache->num_kv_heads).off_flag;
+  uint32_t f = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemcpyAsync(&f, flag, sizeof(f), cudaMemcpyDeviceToHost, st) != cudaSuccess) return JFA_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return JFA_ERR_CUDA;
+  if (flag_out) *flag_out = f;
+  return f ? JFA_ERR_DEVICE : JFA_OK;
 }
 
 int jfa_correct_merge(const jfa_geom* geom, const jfa_cache* cache, const uint16_t* q,

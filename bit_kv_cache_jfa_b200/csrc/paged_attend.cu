@@ -1,0 +1,763 @@
+// paged_attend.cu — jfa_paged_attend: attention of one query token per
+// sequence over the paged 4-bit cache and its bf16 tails, whole or through a
+// sliding window with the first tokens kept.
+//
+//   out[b][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max),
+// over the visible tokens t < n (all, or t >= n - window and t < sinks), the
+// packed ones dequantised: k = s_c k' + m_c (per channel, 64 tokens),
+// v = s_j v' + m_j (per token and 32 channels).
+//
+// What bounds it: the cache is read once, 152 B per packed token and KV head,
+// for 4 * 128 * G flop, far under the tensor rate: HBM, if the SM keeps up
+// with unpacking 4-bit codes.  So the codes never leave the registers of the
+// warp that loads them: they are stored in the order of the mma.sync
+// fragments, one AND turns a 32-bit word into a ready fp16 operand (subnormal
+// code * 2^(pos - 24), exact), and the scales go to the other operand:
+//   logits  A = key codes (16 tokens x 16 channels),
+//           B = fp16(q_c s_c) of the KV head's <= 8 query heads;
+//   values  A = value codes (16 channels x 16 tokens), B = fp16(p_t s_tj).
+//
+// Rounding q_c s_c to fp16 errs by d_c, |d_c| <= 2^-11 |q_c s_c|.  A code is
+// 7.5 + (k' - 7.5), so the part of the error that all 64 tokens share is
+// 7.5 sum_c d_c: it is computed (one chain of 8 MMAs on the remainders) and
+// added.  What is left, sum_c d_c (k'_c - 7.5), is of the size that rounding
+// p_t to fp16 has as well: about 3e-4 of a weight at unit-normal data with
+// outlier channels, against 2^-9 of the bf16 output.  A second fp16 limb of
+// q s would double the key MMAs of a group (32 of 84).
+// The query is scaled by a power of two to [1/8, 1/4) first, so that q s,
+// times the 16 of the codes' position, stays in fp16's range at every scale a
+// record can hold (131008 / 15).  The weights are taken against a reference
+// 2^e under the running maximum, p_t = 2^(u - max + e): e is 15 where the
+// value scales are below 2 and falls (for the rest of the segment) where a
+// larger one would take p_t s_tj past fp16, so that weights down to 2^-29 of
+// the largest keep their 11 bits, however many tokens share the mass.
+#include "jfa_approx.cuh"
+#include "jfa_paged.cuh"
+
+namespace jfa {
+
+constexpr int kPaThreads = 32 * kPgWarps;
+constexpr int kPaK = 512 + 4096;   // key scales, zero points and codes
+constexpr int kPaV = 1024 + 4096;  // the same of the values
+// Per warp two key buffers and one value buffer: while the values of a group
+// are used the next keys have arrived, and while keys are used the values
+// arrive.  16 warps hold about 150 KB in flight per SM.
+constexpr int kPaWarpBytes = 2 * kPaK + kPaV;
+constexpr int kPaSmem = kPgWarps * kPaWarpBytes;
+constexpr int kPaTailTok = 16;                      // tokens of a tail item
+constexpr int kPaTailBytes = kPaTailTok * kPgRow;   // of K or V
+constexpr int kPaMinItems = 8;                      // items per CTA, at least
+static_assert(kPaTailBytes <= kPaK && kPaTailBytes <= kPaV, "a tail item fits the buffers");
+static_assert(kPgPart * 4 <= kPaWarpBytes, "a warp's partial fits its buffers");
+static_assert(kPaSmem + 3072 <= 227 * 1024, "shared memory");
+constexpr float kPaLn2 = 0.6931471805599453f;
+// Where a running maximum starts: finite, so that a masked logit (-inf) minus
+// it is -inf and its weight 0.
+constexpr float kPaMin = -1e30f;
+
+struct PagedAttendParams {
+  jfa_paged c;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  float* part_cta;   // [grid][2][8][132]
+  float* part_warp;  // [grid][16][8][132]
+  uint32_t* ticket;  // [batch][H_kv]
+  uint32_t* flag;
+  int64_t q_row;
+  int G, window, sinks;
+  float kappa;  // scale * log2(e)
+};
+
+// What a sequence of n tokens shows and how it is cut into items: the groups
+// with kept first tokens, the groups from the window on, then the tail, 16
+// tokens an item.
+struct RowView {
+  int n, nq, win_lo, sink_end;  // visible: t < sink_end or win_lo <= t < n
+  int gs, gw, ng, tq0, items;   // groups [0, gs) and [gw, ng), tail items from tq0 on
+};
+__device__ __forceinline__ RowView row_view(int n, int window, int sinks) {
+  RowView v;
+  v.n = n;
+  v.nq = split_point(n);
+  v.win_lo = window > 0 ? max(n - window, 0) : 0;
+  v.sink_end = min(sinks, v.win_lo);
+  v.ng = v.nq / kKG;
+  v.gw = min(v.win_lo / kKG, v.ng);
+  v.gs = min((v.sink_end + kKG - 1) / kKG, v.gw);
+  v.tq0 = v.sink_end > v.nq ? 0 : max(v.win_lo - v.nq, 0) / kPaTailTok;
+  v.items = v.gs + (v.ng - v.gw) + (n - v.nq + kPaTailTok - 1) / kPaTailTok - v.tq0;
+  return v;
+}
+
+enum : int { kItTail = 1, kItMask = 2, kItSkip = 4, kItFirst = 8, kItLast = 16 };
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t a[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t a[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// 16-bit halves kept for the visible ones of two tokens.
+__device__ __forceinline__ uint32_t half_mask(bool lo, bool hi) {
+  return (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+}
+
+// Persistent: the items of all (sequence, KV head) segments, in a row, are cut
+// into equal ranges, one per CTA and in it one per warp.  A warp carries the
+// running maximum, mass and weighted values of its current segment; what it
+// finishes alone it writes out, the rest is merged in fixed order (so results
+// do not depend on timing): over the CTA's warps in shared memory, over CTAs
+// by the last one to add its items to the segment's ticket.
+__global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __grid_constant__ PagedAttendParams p) {
+  extern __shared__ __align__(128) uint8_t pa_smem[];
+  __shared__ int pre[kMaxBatch + 1];
+  __shared__ int wsum[kMaxBatch / 32];
+  __shared__ uint64_t bars[kPgWarps][3];
+  __shared__ int tail_seg[kPgWarps + 1], head_seg[kPgWarps + 1];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
+  const int hkv = p.c.num_kv_heads, G = p.G, H = p.c.num_heads;
+  uint8_t* ring = pa_smem + warp * kPaWarpBytes;
+  uint64_t* bar_k = bars[warp];
+  uint64_t* bar_v = &bars[warp][2];
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) mbar_init(&bars[warp][i], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  {
+    int items = 0;
+    if (tid < p.c.batch) {
+      const int n = checked_len(p.c.seq_lens[tid], p.c.max_pages, p.flag);
+      items = row_view(n, p.window, p.sinks).items * hkv;
+    }
+    batch_prefix(items, pre, wsum);
+  }
+  auto row_of = [&](int row) {
+    return row_view(checked_len(p.c.seq_lens[row], p.c.max_pages, nullptr), p.window, p.sinks);
+  };
+  const int T = pre[kMaxBatch];
+  // sequences that show nothing: zeros, spread over the CTAs
+  for (int row = blockIdx.x; row < p.c.batch; row += gridDim.x) {
+    if (pre[row + 1] != pre[row]) continue;
+    for (int i = tid; i < H * (kD / 8); i += kPaThreads)
+      *reinterpret_cast<uint4*>(p.out + (size_t)row * H * kD + 8 * i) = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = tid; i < H; i += kPaThreads) p.lse[(size_t)row * H + i] = -INFINITY;
+  }
+  const int C = min((int)gridDim.x, (T + kPaMinItems - 1) / kPaMinItems);
+  if ((int)blockIdx.x >= C) return;
+  const int r0 = (int)((long long)blockIdx.x * T / C), r1 = (int)((long long)(blockIdx.x + 1) * T / C);
+  const int nw = min(kPgWarps, r1 - r0);  // the first nw warps have items
+  const int i0 = warp < nw ? r0 + (int)((long long)(r1 - r0) * warp / nw) : r1;
+  const int i1 = warp < nw ? r0 + (int)((long long)(r1 - r0) * (warp + 1) / nw) : r1;
+
+  // ---- item descriptors: lane l holds those of item base + l
+  int base = i0;
+  size_t d_off = 0;  // byte offset in the pages (or in the tails)
+  int d_seg = 0, d_t0 = 0, d_kind = 0;
+  auto describe = [&]() {
+    const int x = base + lane;
+    if (x < i1) {
+      const int row = batch_find(pre, x);
+      const RowView v = row_of(row);
+      const int rel = x - pre[row], head = rel / v.items, j = rel % v.items;
+      d_seg = row * hkv + head;
+      d_kind = (j == 0 ? kItFirst : 0) | (j == v.items - 1 ? kItLast : 0);
+      const int npk = v.gs + v.ng - v.gw;
+      if (j < npk) {
+        const int g = j < v.gs ? j : v.gw + j - v.gs;
+        d_t0 = g * kKG;
+        if (d_t0 < v.win_lo && d_t0 + kKG > v.sink_end) d_kind |= kItMask;
+        int page = p.c.table[(size_t)row * p.c.max_pages + g];
+        if (page < 0 || page >= p.c.n_pages) {
+          set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
+          page = 0;
+          d_kind |= kItSkip | kItMask;
+        }
+        d_off = ((size_t)page * hkv + head) * kPgRec;
+      } else {
+        const int tq = v.tq0 + j - npk;
+        d_t0 = v.nq + tq * kPaTailTok;
+        d_kind |= kItTail;
+        if (d_t0 + kPaTailTok > v.n || (d_t0 < v.win_lo && d_t0 + kPaTailTok > v.sink_end)) d_kind |= kItMask;
+        d_off = (size_t)d_seg * kPgTailBytes + tq * kPaTailBytes;
+      }
+    }
+  };
+  // the lane that holds an item's descriptor requests its copies
+  const uint64_t pol = policy_evict_first();
+  auto issue_k = [&](int x, int st) {
+    if (lane == x - base) {
+      const bool tl = (d_kind & kItTail) != 0;
+      const uint8_t* src = (tl ? reinterpret_cast<const uint8_t*>(p.c.tail_k) : static_cast<const uint8_t*>(p.c.pages)) + d_off;
+      const uint32_t bytes = tl ? kPaTailBytes : kPaK;
+      mbar_expect_tx(&bar_k[st], bytes);
+      bulk_g2s(ring + st * kPaK, src, bytes, &bar_k[st], pol);
+    }
+  };
+  auto issue_v = [&](int x) {
+    if (lane == x - base) {
+      const bool tl = (d_kind & kItTail) != 0;
+      const uint8_t* src = (tl ? reinterpret_cast<const uint8_t*>(p.c.tail_v)
+                               : static_cast<const uint8_t*>(p.c.pages) + kPaK) + d_off;
+      const uint32_t bytes = tl ? kPaTailBytes : kPaV;
+      mbar_expect_tx(bar_v, bytes);
+      bulk_g2s(ring + 2 * kPaK, src, bytes, bar_v, pol);
+    }
+  };
+
+  // ---- state of the current segment; lane (gid, tig): heads 2 tig, 2 tig + 1
+  float acc[8][4];   // values, channels 16 mt + gid (+ 8), at the codes' scale 2^(pos - 24)
+  float dz[4];       // rows 0-3: zero-point sums per channel group, row 4: mass
+  float m_run[2], kap[2];  // reference (running maximum - sh), kappa * 2^x of the query's scaling
+  int sh = 15;             // e of the weights' reference
+  uint32_t q2[16];   // B fragment of the scaled query, head gid
+  int seg = 0;
+  bool own_start = false;  // the segment's first item was this warp's
+  RowView rv;
+  int my_head_seg = -1, my_tail_seg = -1;
+
+  auto reset = [&](int s) {
+    seg = s;
+    const int row = s / hkv, head = s % hkv;
+    rv = row_of(row);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    dz[0] = dz[1] = dz[2] = dz[3] = 0.f;
+    m_run[0] = m_run[1] = kPaMin;
+    sh = 15;
+    const bool ok = gid < G;
+    const uint16_t* qr = p.q + (int64_t)row * p.q_row + (size_t)(head * G + (ok ? gid : 0)) * kD;
+    uint32_t w[16];
+    uint32_t mx = 0u;  // largest magnitude, as bits
+#pragma unroll
+    for (int pp = 0; pp < 16; ++pp) {
+      w[pp] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * (pp >> 1) + 2 * tig + 8 * (pp & 1)) : 0u;
+      mx = max(mx, max(w[pp] << 16, w[pp]) & 0x7FFF0000u);
+      mx = max(mx, max((w[pp] << 16) & 0x7FFF0000u, w[pp] & 0x7FFF0000u));
+    }
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    // 2^(x - 3) <= max|q| < 2^(x - 2); a zero, subnormal or overflowing query is left as it is
+    const int ex = (int)(mx >> 23);
+    const int x = ex == 0 || ex >= 250 ? 0 : ex - 127 + 3;
+    const float down = __uint_as_float((uint32_t)(127 - x) << 23), up = __uint_as_float((uint32_t)(127 + x) << 23);
+#pragma unroll
+    for (int pp = 0; pp < 16; ++pp) q2[pp] = pack_h2(bf_lo(w[pp]) * down, bf_hi(w[pp]) * down);
+    kap[0] = p.kappa * __shfl_sync(0xFFFFFFFFu, up, 8 * tig);
+    kap[1] = p.kappa * __shfl_sync(0xFFFFFFFFu, up, 8 * tig + 4);
+  };
+
+  // the segment's sums out of the registers: dst[h * stride + ...] = m, l, acc
+  auto store_partial = [&](float* dst) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float l = __shfl_sync(0xFFFFFFFFu, dz[e], 16 + tig);
+      float zj[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) zj[j] = __shfl_sync(0xFFFFFFFFu, dz[e], j * 4 + tig);
+      const int h = 2 * tig + e;
+      if (h < G) {
+        float* row = dst + h * kPartStride;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          const float us = (mt >> 2) ? 1048576.0f : 16777216.0f;
+          row[4 + 16 * mt + gid] = fmaf(acc[mt][e], us, zj[mt >> 1]);
+          row[4 + 16 * mt + gid + 8] = fmaf(acc[mt][2 + e], us, zj[mt >> 1]);
+        }
+        if (gid == 0) {
+          row[0] = m_run[e];
+          row[1] = l;
+        }
+      }
+    }
+  };
+  auto store_out = [&]() {
+    const int row = seg / hkv, head = seg % hkv;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float l = __shfl_sync(0xFFFFFFFFu, dz[e], 16 + tig);
+      float zj[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) zj[j] = __shfl_sync(0xFFFFFFFFu, dz[e], j * 4 + tig);
+      const int h = 2 * tig + e;
+      if (h < G) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // only skipped pages: zeros
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)row * H + head * G + h) * kD;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          const float us = (mt >> 2) ? 1048576.0f : 16777216.0f;
+          o[16 * mt + gid] = __float2bfloat16_rn(fmaf(acc[mt][e], us, zj[mt >> 1]) * inv);
+          o[16 * mt + gid + 8] = __float2bfloat16_rn(fmaf(acc[mt][2 + e], us, zj[mt >> 1]) * inv);
+        }
+        if (gid == 0 && p.lse) p.lse[(size_t)row * H + head * G + h] = l == 0.f ? -INFINITY : (m_run[e] + log2f(l)) * kPaLn2;
+      }
+    }
+  };
+  // everything summed so far, to the references n0, n1 (at or above m_run)
+  auto rescale = [&](float n0, float n1) {
+    const float a0 = approx_weight(m_run[0], n0), a1 = approx_weight(m_run[1], n1);
+    m_run[0] = n0;
+    m_run[1] = n1;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      acc[mt][0] *= a0;
+      acc[mt][1] *= a1;
+      acc[mt][2] *= a0;
+      acc[mt][3] *= a1;
+    }
+    dz[0] *= a0;
+    dz[1] *= a1;
+    dz[2] *= a0;
+    dz[3] *= a1;
+  };
+  // the lane's largest logits of heads 2 tig + e: raises the references
+  auto raise_max = [&](float mx0, float mx1) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, o));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, o));
+    }
+    mx0 -= (float)sh;
+    mx1 -= (float)sh;
+    if (__any_sync(0xFFFFFFFFu, mx0 > m_run[0] || mx1 > m_run[1]))
+      rescale(fmaxf(m_run[0], mx0), fmaxf(m_run[1], mx1));
+  };
+
+  if (i0 < i1) {
+    describe();
+    __syncwarp();
+    issue_k(i0, 0);
+    issue_v(i0);
+    if (i0 + 1 < i1) issue_k(i0 + 1, 1);
+  }
+  int st = 0;
+  uint32_t par_k = 0u, par_v = 0u;  // bit s: parity of key buffer s
+  bool failed = false;
+  for (int i = i0; i < i1; ++i) {
+    if (i + 2 - base >= 32 && i + 2 < i1) {  // the next keys' descriptor is needed below
+      base = i;
+      describe();
+      __syncwarp();
+    }
+    const int kind = __shfl_sync(0xFFFFFFFFu, d_kind, i - base);
+    const int t0 = __shfl_sync(0xFFFFFFFFu, d_t0, i - base);
+    {
+      const int s = __shfl_sync(0xFFFFFFFFu, d_seg, i - base);
+      if (i == i0 || (kind & kItFirst)) {
+        reset(s);
+        own_start = (kind & kItFirst) != 0;
+      }
+    }
+    auto visible = [&](int t) {
+      return !(kind & kItSkip) && t < rv.n && (t >= rv.win_lo || t < rv.sink_end);
+    };
+    failed |= !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar_k[st], (par_k >> st) & 1u));
+    par_k ^= 1u << st;
+    const uint8_t* rk = ring + st * kPaK;
+    const uint8_t* rvb = ring + 2 * kPaK;
+    if (!(kind & kItTail)) {
+      // ---- B operand fp16(q s F), the remainders' share and the bias
+      uint32_t qb[16];
+      float bk[2];
+      {
+        uint32_t sk[16], zk[16];
+        key_sz(rk, tig, sk, zk);
+        float bz[4] = {0.f, 0.f, 0.f, 0.f}, cr[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma16816(bz, zk[2 * ks], zk[2 * ks], zk[2 * ks + 1], zk[2 * ks + 1], q2[2 * ks], q2[2 * ks + 1]);
+        uint32_t lo[16];
+#pragma unroll
+        for (int pp = 0; pp < 16; ++pp) {
+          const uint32_t qf = h2_mul(q2[pp], KeyPos<4>::factor(pp));
+          qb[pp] = h2_mul(qf, sk[pp]);
+          lo[pp] = h2_fma(qf, sk[pp], qb[pp] ^ 0x80008000u);
+        }
+        // twice 7.5, at the codes' bit position: 0 for slots 0-7, 4 for 8-15
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t c15 = ks < 4 ? 0x000F000Fu : 0x00F000F0u;
+          mma16816(cr, c15, c15, c15, c15, lo[2 * ks], lo[2 * ks + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) bk[e] = fmaf(cr[e], 0.5f * KeyPos<4>::unscale, bz[e]) * kap[e];
+      }
+      // ---- logits (log2 units) u[mt][2 r + e]: token 16 mt + gid + 8 r, head 2 tig + e
+      float u[4][4];
+      const float ku[2] = {kap[0] * KeyPos<4>::unscale, kap[1] * KeyPos<4>::unscale};
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const uint8_t* kp = rk + 512 + mt * 1024 + lane * 32;
+        const uint4 c0 = *reinterpret_cast<const uint4*>(kp), c1 = *reinterpret_cast<const uint4*>(kp + 16);
+        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        uint32_t a[16][2];
+        key_afrag<4>(w, a);
+        float d[4];
+        qk_chain(a, qb, d);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) u[mt][x] = fmaf(d[x], ku[x & 1], bk[x & 1]);
+      }
+      __syncwarp();
+      if (i + 2 < i1) issue_k(i + 2, st);
+      if (kind & kItMask) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (!visible(t0 + 16 * mt + gid + 8 * (x >> 1))) u[mt][x] = -INFINITY;
+      }
+      float mx0 = u[0][0], mx1 = u[0][1];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        mx0 = fmaxf(mx0, fmaxf(u[mt][0], u[mt][2]));
+        mx1 = fmaxf(mx1, fmaxf(u[mt][1], u[mt][3]));
+      }
+      raise_max(mx0, mx1);
+      // ---- weights, fp16, as the values' B operand (tokens down, head gid)
+      uint32_t pa[4], pb[4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        pa[mt] = movmatrix_trans(pack_h2(approx_weight(u[mt][0], m_run[0]), approx_weight(u[mt][1], m_run[1])));
+        pb[mt] = movmatrix_trans(pack_h2(approx_weight(u[mt][2], m_run[0]), approx_weight(u[mt][3], m_run[1])));
+      }
+      failed |= !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_v, par_v));
+      par_v ^= 1u;
+      {  // the group's largest value scale: 2^k <= s < 2^(k + 1) allows sh <= 15 - k
+        const uint4 sw = *reinterpret_cast<const uint4*>(rvb + lane * 16);
+        const uint32_t s2 = __vmaxu2(__vmaxu2(sw.x, sw.y), __vmaxu2(sw.z, sw.w));
+        const uint32_t smax = __reduce_max_sync(0xFFFFFFFFu, max(s2 & 0xFFFFu, s2 >> 16));
+        const int fit = max(30 - (int)(smax >> 10), 0);
+        if (fit < sh) {
+          const float d = (float)(sh - fit);
+          sh = fit;
+          rescale(m_run[0] + d, m_run[1] + d);
+          const uint32_t down = pack_h2(exp2f(-d), exp2f(-d));
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            pa[mt] = h2_mul(pa[mt], down);
+            pb[mt] = h2_mul(pb[mt], down);
+          }
+        }
+      }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint4 s0 = *reinterpret_cast<const uint4*>(rvb + kk * 128 + tig * 32);
+        const uint4 s1 = *reinterpret_cast<const uint4*>(rvb + kk * 128 + tig * 32 + 16);
+        uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        uint32_t za0 = gid == 4 ? kOneH2 : 0u, za2 = za0;
+        if (gid < 4) {
+          const uint2 zz = *reinterpret_cast<const uint2*>(rvb + 512 + kk * 128 + tig * 32 + gid * 8);
+          za0 = zz.x;
+          za2 = zz.y;
+        }
+        if (kind & kItMask) {  // what a masked token holds does not matter, infinities too
+          const int t = t0 + 16 * kk + 2 * tig;
+          const uint32_t ma = half_mask(visible(t), visible(t + 1)), mb = half_mask(visible(t + 8), visible(t + 9));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sv[2 * j] &= ma;
+            sv[2 * j + 1] &= mb;
+          }
+          za0 &= ma;
+          za2 &= mb;
+        }
+        uint32_t bh[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bh[j][0] = h2_mul(pa[kk], sv[2 * j]);
+          bh[j][1] = h2_mul(pb[kk], sv[2 * j + 1]);
+        }
+        mma16816(dz, za0, 0u, za2, 0u, pa[kk], pb[kk]);
+        const uint4 v0 = *reinterpret_cast<const uint4*>(rvb + 1024 + (2 * kk) * 512 + lane * 16);
+        const uint4 v1 = *reinterpret_cast<const uint4*>(rvb + 1024 + (2 * kk + 1) * 512 + lane * 16);
+        const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t vs[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) vs[x] = vw[x] >> 8;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          const int w = mt & 3;
+          const uint32_t mask = 0x000F000Fu << (4 * (mt >> 2));
+          mma16816(acc[mt], vw[2 * w] & mask, vs[2 * w] & mask, vw[2 * w + 1] & mask, vs[2 * w + 1] & mask,
+                   bh[mt >> 1][0], bh[mt >> 1][1]);
+        }
+      }
+    } else {
+      // ---- 16 tail tokens, exact bf16 rows: keys are A rows as they lie
+      uint32_t qw[16];
+      {
+        const bool ok = gid < G;
+        const uint16_t* qr = p.q + (int64_t)(seg / hkv) * p.q_row + (size_t)((seg % hkv) * G + (ok ? gid : 0)) * kD;
+#pragma unroll
+        for (int pp = 0; pp < 16; ++pp)
+          qw[pp] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * (pp >> 1) + 2 * tig + 8 * (pp & 1)) : 0u;
+      }
+      const int mi = lane >> 3, r = lane & 7;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        uint32_t a[4];
+        ldmatrix4(a, smem_u32(rk) + tail_chunk(r + 8 * (mi & 1), 2 * ks + (mi >> 1)));
+        mma_bf16(d, a[0], a[1], a[2], a[3], qw[2 * ks], qw[2 * ks + 1]);
+      }
+      __syncwarp();
+      if (i + 2 < i1) issue_k(i + 2, st);
+      float u[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) u[x] = visible(t0 + gid + 8 * (x >> 1)) ? d[x] * p.kappa : -INFINITY;
+      raise_max(fmaxf(u[0], u[2]), fmaxf(u[1], u[3]));
+      // weights as a bf16 high part and its remainder (16 bits together)
+      uint32_t ph[2], pl[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float w0 = approx_weight(u[2 * x], m_run[0]), w1 = approx_weight(u[2 * x + 1], m_run[1]);
+        const uint32_t hi = pack_b2(w0, w1);
+        ph[x] = movmatrix_trans(hi);
+        pl[x] = movmatrix_trans(pack_b2(w0 - bf_lo(hi), w1 - bf_hi(hi)));
+      }
+      failed |= !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_v, par_v));
+      par_v ^= 1u;
+      const uint32_t one = gid == 4 ? 0x3F803F80u : 0u;
+      mma_bf16(dz, one, 0u, one, 0u, ph[0], ph[1]);
+      mma_bf16(dz, one, 0u, one, 0u, pl[0], pl[1]);
+      const uint32_t ma = half_mask(visible(t0 + 2 * tig), visible(t0 + 2 * tig + 1));
+      const uint32_t mb = half_mask(visible(t0 + 2 * tig + 8), visible(t0 + 2 * tig + 9));
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        uint32_t a[4];
+        ldmatrix4_trans(a, smem_u32(rvb) + tail_chunk(r + 8 * (mi >> 1), 2 * mt + (mi & 1)));
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_bf16(o, a[0] & ma, a[1] & ma, a[2] & mb, a[3] & mb, ph[0], ph[1]);
+        mma_bf16(o, a[0] & ma, a[1] & ma, a[2] & mb, a[3] & mb, pl[0], pl[1]);
+        const float ps = (mt >> 2) ? 0x1p-20f : 0x1p-24f;  // to the accumulator's scale
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[mt][x] = fmaf(o[x], ps, acc[mt][x]);
+      }
+    }
+    __syncwarp();
+    if (i + 1 < i1) issue_v(i + 1);
+    st ^= 1;
+    if (kind & kItLast) {
+      if (own_start) {
+        store_out();
+      } else {
+        store_partial(p.part_warp + ((size_t)blockIdx.x * kPgWarps + warp) * kPgPart);
+        my_head_seg = seg;
+      }
+    } else if (i == i1 - 1) {
+      my_tail_seg = seg;
+      __syncwarp();
+      store_partial(reinterpret_cast<float*>(ring));  // every copy has been used
+    }
+  }
+  if (failed && lane == 0) set_flag(p.flag, JFA_DEVERR_TIMEOUT);
+  if (lane == 0) {
+    tail_seg[warp] = my_tail_seg;
+    head_seg[warp] = my_head_seg;
+    if (warp == 0) tail_seg[kPgWarps] = head_seg[kPgWarps] = -1;
+  }
+  __syncthreads();
+
+  // ---- merge over the CTA's warps.  Runs: a segment's warps w .. e - 1 that
+  // hold it last, and warp e if it ended there; the first warp may also have
+  // ended a segment of the CTA before.  A warp takes a (run, head) at a time,
+  // a lane 4 channels.
+  auto seg_range = [&](int s, int& sa, int& sb) {
+    const int row = s / hkv, items = (pre[row + 1] - pre[row]) / hkv;
+    sa = pre[row] + (s % hkv) * items;
+    sb = sa + items;
+  };
+  auto smem_part = [&](int w) { return reinterpret_cast<const float*>(pa_smem + w * kPaWarpBytes); };
+  auto gmem_part = [&](int w) { return p.part_warp + ((size_t)blockIdx.x * kPgWarps + w) * kPgPart; };
+  auto finish = [&](int s, int h, float M, float L, float4 O) {
+    const int row = s / hkv, head = s % hkv;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t at = (size_t)row * H + head * G + h;
+    *reinterpret_cast<uint2*>(p.out + at * kD + 4 * lane) =
+        make_uint2(pack_b2(O.x * inv, O.y * inv), pack_b2(O.z * inv, O.w * inv));
+    if (lane == 0 && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPaLn2;
+  };
+  for (int c = warp; c < (kPgWarps + 1) * G; c += kPgWarps) {
+    const int run = c / G, h = c % G;  // run 0: warp 0's ended segment; run w + 1 begins at warp w
+    int s, w0, w1, wh;                 // shared partials w0 .. w1 - 1 and, if wh >= 0, warp wh's in the workspace
+    if (run == 0) {
+      s = head_seg[0];
+      w0 = w1 = 0;
+      wh = 0;
+    } else {
+      w0 = run - 1;
+      s = tail_seg[w0];
+      if (w0 > 0 && tail_seg[w0 - 1] == s) s = -1;
+      w1 = w0 + 1;
+      while (w1 < kPgWarps && tail_seg[w1] == s) ++w1;
+      wh = head_seg[w1] == s ? w1 : -1;
+    }
+    if (s < 0) continue;
+    float M = kPaMin;
+    for (int w = w0; w < w1; ++w) M = fmaxf(M, smem_part(w)[h * kPartStride]);
+    if (wh >= 0) M = fmaxf(M, gmem_part(wh)[h * kPartStride]);
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float* src) {
+      const float f = exp2f(src[0] - M);
+      const float4 v = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
+      L = fmaf(src[1], f, L);
+      O.x = fmaf(v.x, f, O.x);
+      O.y = fmaf(v.y, f, O.y);
+      O.z = fmaf(v.z, f, O.z);
+      O.w = fmaf(v.w, f, O.w);
+    };
+    for (int w = w0; w < w1; ++w) add(smem_part(w) + h * kPartStride);
+    if (wh >= 0) add(gmem_part(wh) + h * kPartStride);
+    int sa, sb;
+    seg_range(s, sa, sb);
+    if (sa >= r0 && sb <= r1) {
+      finish(s, h, M, L, O);
+    } else {
+      float* dst = p.part_cta + ((size_t)blockIdx.x * 2 + (sa < r0 ? 0 : 1)) * kPgPart + h * kPartStride;
+      if (lane == 0) {
+        dst[0] = M;
+        dst[1] = L;
+      }
+      *reinterpret_cast<float4*>(dst + 4 + 4 * lane) = O;
+    }
+  }
+
+  // ---- the segments at the range's ends that other CTAs share
+  __threadfence();
+  __syncthreads();
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {
+    const int x = end == 0 ? r0 : r1 - 1;
+    const int row = batch_find(pre, x), items = (pre[row + 1] - pre[row]) / hkv;
+    const int s = row * hkv + (x - pre[row]) / items;
+    int sa, sb;
+    seg_range(s, sa, sb);
+    if (sa >= r0 && sb <= r1) continue;      // finished here
+    if (end == 1 && sa <= r0) continue;      // one segment fills the range
+    if (tid == 0) {
+      const uint32_t mine = (uint32_t)(min(sb, r1) - max(sa, r0));
+      s_last = atomicAdd(&p.ticket[s], mine) + mine == (uint32_t)(sb - sa);
+    }
+    __syncthreads();
+    const bool last = s_last != 0;
+    __syncthreads();
+    if (!last) continue;
+    __threadfence();
+    const int ca = (int)(((long long)(sa + 1) * C - 1) / T), cb = (int)(((long long)sb * C - 1) / T);
+    // G heads, 16 / G warps each on every so-manieth CTA's partial
+    const int per = kPgWarps / G, h = warp % G, sub = warp / G;
+    auto part = [&](int c) {
+      const int rc = (int)((long long)c * T / C);
+      return p.part_cta + ((size_t)c * 2 + (sa < rc ? 0 : 1)) * kPgPart + h * kPartStride;
+    };
+    float* buf = reinterpret_cast<float*>(pa_smem) + warp * kPartStride;
+    if (sub < per) {
+      float M = kPaMin;
+      for (int c = ca + sub + per * lane; c <= cb; c += per * 32) M = fmaxf(M, __ldcg(part(c)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+      float L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = ca + sub; c <= cb; c += per) {
+        const float* src = part(c);
+        const float f = exp2f(__ldcg(src) - M);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + 4 + 4 * lane));
+        L = fmaf(__ldcg(src + 1), f, L);
+        O.x = fmaf(v.x, f, O.x);
+        O.y = fmaf(v.y, f, O.y);
+        O.z = fmaf(v.z, f, O.z);
+        O.w = fmaf(v.w, f, O.w);
+      }
+      if (lane == 0) {
+        buf[0] = M;
+        buf[1] = L;
+      }
+      *reinterpret_cast<float4*>(buf + 4 + 4 * lane) = O;
+    }
+    __syncthreads();
+    if (warp < G) {
+      float M = kPaMin;
+      for (int i = 0; i < per; ++i) M = fmaxf(M, reinterpret_cast<const float*>(pa_smem)[(h + i * G) * kPartStride]);
+      float L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < per; ++i) {
+        const float* src = reinterpret_cast<const float*>(pa_smem) + (h + i * G) * kPartStride;
+        const float f = exp2f(src[0] - M);
+        const float4 v = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
+        L = fmaf(src[1], f, L);
+        O.x = fmaf(v.x, f, O.x);
+        O.y = fmaf(v.y, f, O.y);
+        O.z = fmaf(v.z, f, O.z);
+        O.w = fmaf(v.w, f, O.w);
+      }
+      finish(s, h, M, L, O);
+    }
+    if (tid == 0) p.ticket[s] = 0u;
+    __syncthreads();
+  }
+}
+
+int launch_paged_attend(const jfa_paged& c, const uint16_t* q, int64_t q_row, float scale, int window,
+                        int sinks, uint8_t* ws, uint16_t* out, float* lse, cudaStream_t st) {
+  const PagedWs w = paged_ws(c.batch, c.num_kv_heads);
+  PagedAttendParams p;
+  p.c = c;
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.part_cta = reinterpret_cast<float*>(ws + w.off_cta);
+  p.part_warp = reinterpret_cast<float*>(ws + w.off_warp);
+  p.ticket = reinterpret_cast<uint32_t*>(ws + w.off_ticket);
+  p.flag = reinterpret_cast<uint32_t*>(ws + w.off_flag);
+  p.q_row = q_row;
+  p.G = c.num_heads / c.num_kv_heads;
+  p.window = window;
+  p.sinks = sinks;
+  p.kappa = scale * 1.4426950408889634f;
+  static bool configured[64] = {false};  // per device: the attribute is set on each
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return JFA_ERR_CUDA;
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    if (cudaFuncSetAttribute(paged_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPaSmem) != cudaSuccess)
+      return JFA_ERR_CUDA;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  const int sms = num_sms_current();
+  return launch_pdl(paged_attend_kernel, dim3(sms < kPgMaxCtas ? sms : kPgMaxCtas), dim3(kPaThreads), (size_t)kPaSmem,
+                    st, p) == cudaSuccess
+             ? JFA_OK
+             : JFA_ERR_CUDA;
+}
+
+}  // namespace jfa

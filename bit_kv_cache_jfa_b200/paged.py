@@ -1,0 +1,487 @@
+"""The paged 4-bit cache and the head norms and rotary positions in front of
+it: argument checks, device buffers and the host's page book-keeping over the
+jfa_paged_* and jfa_qk_norm_rope calls.
+
+    table = PageTable(batch, n_pages, max_pages)        # one for all layers
+    cache = PagedKVCache(table, heads, kv_heads)        # one per layer
+    ws = PagedWorkspace(cache)
+    cu = table.grow([700, 1300])                        # prompts enter
+    paged_append(cache, k, v, ws, cu)
+    table.grow(1)                                       # then a token each
+    out = paged_decode_step(cache, q, k, v, table.seq_lens - 1, plan, ws)
+
+Unlike the calls on contiguous caches, these launch on torch's current stream
+when no stream is given, and on the device that holds the cache.
+"""
+from __future__ import annotations
+
+import contextlib
+import heapq
+import math
+
+from . import _lib
+from ._lib import JFA_ERR_INVALID_ARG, JfaError, Paged, Rope, check
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _refuse(where: str, why: str):
+    raise JfaError(JFA_ERR_INVALID_ARG, f"{where}: {why}")
+
+
+def _on(dev, stream):
+    """(guard that makes dev current, stream handle) of a call."""
+    cuda = _torch().cuda
+    guard = _NO_GUARD if cuda.current_device() == dev.index else cuda.device(dev)
+    if stream is None:
+        stream = cuda.current_stream(dev)
+    return guard, stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _int32(x, n, dev, where, name):
+    torch = _torch()
+    if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous() or x.device != dev:
+        _refuse(where, f"{name} must be {n} contiguous int32 on {dev}")
+    return x.data_ptr()
+
+
+def _rows(x, heads, dev, where, name):
+    """Address and strides of bf16 rows [T][heads][128]."""
+    torch = _torch()
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != _lib.HEAD_DIM \
+            or x.device != dev or (x.stride(2) != 1 and x.numel()):
+        _refuse(where, f"{name} must be bf16 [tokens, {heads}, {_lib.HEAD_DIM}] on {dev}, channels contiguous")
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+def _device(device):
+    torch = _torch()
+    dev = torch.device(device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return dev
+
+
+class RotaryPlan:
+    """Frequencies of the rotary positions of a model, on the device.
+
+    rotary_dim: channels that turn (even, at most 128); interleaved: pairs
+    (2i, 2i + 1) instead of (i, i + rotary_dim / 2).  f_i = base^(-2i / rotary_dim),
+    changed by ``scaling``:
+
+    - "none"
+    - "linear": f / factor
+    - "llama3": f / factor where the wavelength is over original /
+      low_freq_factor, f where it is under original / high_freq_factor, in
+      between a blend that is linear in original / wavelength
+    - "yarn": a blend of f / factor and f that is linear in i between the
+      pairs that make beta_slow and beta_fast turns in the original context;
+      rotated channels grow by amplitude = 0.1 ln(factor) + 1
+
+    ``amplitude`` replaces the scaling's own."""
+
+    def __init__(self, rotary_dim: int = 128, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, low_freq_factor: float = 1.0,
+                 high_freq_factor: float = 4.0, original: int | None = None,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float | None = None,
+                 device="cuda"):
+        where = "RotaryPlan"
+        if rotary_dim % 2 or not 2 <= rotary_dim <= _lib.HEAD_DIM:
+            _refuse(where, f"rotary_dim must be even, in 2..{_lib.HEAD_DIM}")
+        if not base > 1 or not factor > 0:
+            _refuse(where, "base must be above 1 and factor above 0")
+        if scaling not in ("none", "linear", "llama3", "yarn"):
+            _refuse(where, f"unknown scaling {scaling!r}")
+        if scaling in ("llama3", "yarn") and not (original and original > 0):
+            _refuse(where, f"scaling {scaling!r} needs the original context length")
+        if scaling == "llama3" and not high_freq_factor > low_freq_factor:
+            _refuse(where, "high_freq_factor must be above low_freq_factor")
+        if scaling == "yarn" and not beta_fast > beta_slow > 0:
+            _refuse(where, "beta_fast must be above beta_slow, and that above 0")
+        self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
+        half = rotary_dim // 2
+        f = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
+        m = 1.0
+        if scaling == "linear":
+            f = [x / factor for x in f]
+        elif scaling == "llama3":
+            keep = [(original * x / (2 * math.pi) - low_freq_factor) / (high_freq_factor - low_freq_factor)
+                    for x in f]
+            keep = [min(max(u, 0.0), 1.0) for u in keep]
+            f = [x * (u + (1 - u) / factor) for x, u in zip(f, keep)]
+        elif scaling == "yarn":
+            def pair(turns):  # that makes so many turns in the original context
+                return rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo = max(math.floor(pair(beta_fast)), 0)
+            hi = min(math.ceil(pair(beta_slow)), rotary_dim - 1)
+            ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(half)]
+            f = [x * (1 - u + u / factor) for x, u in zip(f, ramp)]
+            m = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+        self.frequencies = tuple(f)          # radians per position
+        self.amplitude = float(m if amplitude is None else amplitude)
+        if not math.isfinite(self.amplitude):
+            _refuse(where, "amplitude must be finite")
+        turns = [round(x / (2 * math.pi) * 2.0**64) % 2**64 for x in f]   # in 2^-64 turns
+        torch = _torch()
+        self.freq = torch.tensor([t - 2**64 if t >= 2**63 else t for t in turns], dtype=torch.int64,
+                                 device=_device(device))
+
+
+def qk_norm_rope(q, k, positions, plan: RotaryPlan, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head (where a weight is given) and
+    rotation by position, in one pass.
+
+    q bf16 [T, H, 128], k bf16 [T, H_kv, 128] (any token and head strides that
+    are multiples of 8, channels contiguous); positions int32 or int64 [T];
+    weights bf16 [128].  Returns (q, k) bf16, contiguous unless given; q_out=q
+    and k_out=k work in place."""
+    torch = _torch()
+    where = "qk_norm_rope"
+    dev = plan.freq.device
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0]:
+        _refuse(where, "q and k must be [tokens, heads, 128] of the same tokens")
+    t, h, hkv = q.shape[0], q.shape[1], k.shape[1]
+    qa, ka = _rows(q, h, dev, where, "q"), _rows(k, hkv, dev, where, "k")
+    wide = positions.dtype == torch.int64
+    if not (wide or positions.dtype == torch.int32) or positions.shape != (t,) or positions.device != dev \
+            or not positions.is_contiguous():
+        _refuse(where, f"positions must be {t} contiguous int32 or int64 on {dev}")
+    w = []
+    for x, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if x is not None and (x.dtype != torch.bfloat16 or x.shape != (_lib.HEAD_DIM,) or x.device != dev
+                              or not x.is_contiguous()):
+            _refuse(where, f"{name} must be bf16 [{_lib.HEAD_DIM}] on {dev}")
+        w.append(None if x is None else x.data_ptr())
+    if q_out is None:
+        q_out = torch.empty((t, h, _lib.HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    if k_out is None:
+        k_out = torch.empty((t, hkv, _lib.HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        _refuse(where, "outputs must have their inputs' shapes")
+    qo, ko = _rows(q_out, h, dev, where, "q_out"), _rows(k_out, hkv, dev, where, "k_out")
+    r = Rope(t, h, hkv, plan.rotary_dim, plan.interleaved, wide, eps, plan.amplitude, qa[0], ka[0], qo[0],
+             ko[0], qa[1], qa[2], ka[1], ka[2], qo[1], qo[2], ko[1], ko[2], w[0], w[1],
+             positions.data_ptr(), plan.freq.data_ptr())
+    guard, st = _on(dev, stream)
+    with guard:
+        check(_lib.jfa_qk_norm_rope(r, st), "jfa_qk_norm_rope")
+    return q_out, k_out
+
+
+class PageTable:
+    """Pages of the sequences of a batch: the device table and lengths that
+    the kernels read, and the host's book of free and shared pages.  Layers
+    with the same sequences share one table (a pool of pages each).
+
+    A page is written when its 64 tokens are complete and never again, so
+    forked sequences share it by count; it is free once no sequence lists it.
+    Updates are enqueued on torch's current stream."""
+
+    def __init__(self, batch: int, n_pages: int, max_pages: int, device="cuda"):
+        torch = _torch()
+        if not 1 <= batch <= _lib.MAX_BATCH or n_pages < 1 or max_pages < 1:
+            _refuse("PageTable", f"batch must be 1..{_lib.MAX_BATCH}, n_pages and max_pages at least 1")
+        self.batch, self.n_pages, self.max_pages = batch, n_pages, max_pages
+        self.device = _device(device)
+        self.table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=self.device)
+        self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=self.device)
+        self.lens = [0] * batch                       # as seq_lens
+        self.rows = [[] for _ in range(batch)]        # pages of each sequence
+        self._refs = [0] * n_pages
+        self._free = list(range(n_pages))             # heap: the lowest page goes out first
+
+    @property
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    @staticmethod
+    def _packed(n: int) -> int:
+        return 0 if n <= 0 else (n - 1) // _lib.KEY_GROUP
+
+    def _check_row(self, row, where):
+        if not 0 <= row < self.batch:
+            _refuse(where, f"sequence {row} of {self.batch}")
+
+    def _up(self, values):
+        """Host ints to the device, ordered on the current stream."""
+        torch = _torch()
+        return torch.tensor(values, dtype=torch.int32).to(self.device, non_blocking=True)
+
+    def _store(self, cells=(), pages=()):
+        """Lengths, and table cells (row * max_pages + entry) with their pages."""
+        m = len(cells)
+        up = self._up([*self.lens, *cells, *pages])
+        self.seq_lens.copy_(up[:self.batch])
+        if m:
+            self.table.view(-1)[up[self.batch:self.batch + m].long()] = up[self.batch + m:]
+
+    def grow(self, n_new):
+        """Room for new tokens: n_new of every sequence that has any (int), or
+        n_new[b] of sequence b.  Lengths grow and the groups that become
+        complete get pages; paged_append then brings the rows.  Returns the
+        rows' ranges (int32 [batch + 1] on the device) for the second form.
+        Without enough free pages or room in a row nothing changes."""
+        torch = _torch()
+        uniform = isinstance(n_new, int)
+        counts = [n_new if n else 0 for n in self.lens] if uniform else [int(n) for n in n_new]
+        if len(counts) != self.batch or min(counts) < 0:
+            _refuse("PageTable.grow", f"needs {self.batch} counts, none negative")
+        need = []
+        for b, n in enumerate(counts):
+            first, last = self._packed(self.lens[b]), self._packed(self.lens[b] + n)
+            if last > self.max_pages:
+                _refuse("PageTable.grow", f"sequence {b} would need {last} of {self.max_pages} pages")
+            need += [(b, g) for g in range(first, last)]
+        if len(need) > len(self._free):
+            _refuse("PageTable.grow", f"{len(need)} pages needed, {len(self._free)} free")
+        cells, pages = [], []
+        for b, g in need:
+            page = heapq.heappop(self._free)
+            self._refs[page] = 1
+            self.rows[b].append(page)
+            cells.append(b * self.max_pages + g)
+            pages.append(page)
+        self.lens = [a + n for a, n in zip(self.lens, counts)]
+        self._store(cells, pages)
+        if uniform:
+            return None
+        return torch.cat((torch.zeros(1, dtype=torch.int32, device=self.device),
+                          self._up(counts).cumsum(0, dtype=torch.int32)))
+
+    def _release(self, row):
+        for page in self.rows[row]:
+            self._refs[page] -= 1
+            if self._refs[page] == 0:
+                heapq.heappush(self._free, page)
+        self.rows[row] = []
+        self.lens[row] = 0
+
+    def free(self, rows) -> None:
+        """Sequences end: their rows become idle (length 0), pages that no
+        other sequence lists become free."""
+        rows = [int(r) for r in rows]
+        for r in rows:
+            self._check_row(r, "PageTable.free")
+        for r in rows:
+            self._release(r)
+        self._store()
+
+    def fork(self, pairs):
+        """Book (parent, child) forks; a child's earlier pages are released.
+        Returns the pairs (int32 [n, 2] on the device) for paged_fork, which
+        every layer's cache then gets."""
+        pairs = [(int(a), int(b)) for a, b in pairs]
+        children = [b for _, b in pairs]
+        for a, b in pairs:
+            self._check_row(a, "PageTable.fork")
+            self._check_row(b, "PageTable.fork")
+        if len(set(children)) != len(children) or set(children) & {a for a, _ in pairs}:
+            _refuse("PageTable.fork", "a child may be no parent and the child of one pair only")
+        for _, b in pairs:
+            self._release(b)
+        for a, b in pairs:
+            self.rows[b] = list(self.rows[a])
+            self.lens[b] = self.lens[a]
+            for page in self.rows[b]:
+                self._refs[page] += 1
+        return self._up([x for p in pairs for x in p]).view(-1, 2)
+
+    def compact(self):
+        """Book the move of the pages in use to the front of the pool.  Returns
+        (moves int32 [m, 2], remap int32 [n_pages]) on the device for
+        paged_move: every layer's cache gets the moves, one of them the remap."""
+        used = [p for p in range(self.n_pages) if self._refs[p]]
+        holes = [p for p in range(len(used)) if not self._refs[p]]
+        goes = list(range(self.n_pages))
+        moves = list(zip(used[len(used) - len(holes):], holes))
+        for a, b in moves:
+            goes[a] = b
+            self._refs[b], self._refs[a] = self._refs[a], 0
+        self.rows = [[goes[p] for p in row] for row in self.rows]
+        self._free = list(range(len(used), self.n_pages))
+        up = self._up([*goes, *(x for m in moves for x in m)])
+        return up[self.n_pages:].view(-1, 2), up[:self.n_pages]
+
+
+class PagedKVCache:
+    """One layer's paged 4-bit cache (device buffers owned by torch, fixed for
+    its life): the pool of pages and the exact tail of each sequence."""
+
+    def __init__(self, table: PageTable, num_heads: int, num_kv_heads: int):
+        torch = _torch()
+        self.table, self.device = table, table.device
+        self.num_heads, self.num_kv_heads = num_heads, num_kv_heads
+        # sizes first: a bad geometry is refused before anything is allocated
+        self._struct = Paged(table.batch, num_heads, num_kv_heads, table.n_pages, table.max_pages)
+        self.workspace_bytes = _lib.jfa_paged_workspace_bytes(self._struct)
+        self.pages = torch.zeros(table.n_pages, num_kv_heads, _lib.PAGE_RECORD_BYTES, dtype=torch.uint8,
+                                 device=self.device)
+        shape = (table.batch, num_kv_heads, _lib.TAIL_MAX, _lib.HEAD_DIM)
+        self.tail_k = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        self.tail_v = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        s = self._struct
+        s.pages, s.tail_k, s.tail_v = (x.data_ptr() for x in (self.pages, self.tail_k, self.tail_v))
+        s.table, s.seq_lens = table.table.data_ptr(), table.seq_lens.data_ptr()
+
+    def struct(self) -> Paged:
+        return self._struct
+
+    def record(self, page: int, head: int) -> bytes:
+        """Host bytes of a page's record of one KV head (jfa_unpack_record decodes it)."""
+        return self.pages[page, head].cpu().numpy().tobytes()
+
+
+class PagedWorkspace:
+    """Scratch of the paged calls on one cache, or on caches of the same sizes.
+    Calls that may run at the same time need one each."""
+
+    def __init__(self, cache: PagedKVCache):
+        torch = _torch()
+        self.buf = torch.zeros(cache.workspace_bytes, dtype=torch.uint8, device=cache.device)
+
+    def error_flag(self, cache: PagedKVCache, stream=None) -> int:
+        guard, st = _on(cache.device, stream)
+        with guard:
+            status, flag = _lib.jfa_paged_check_error(cache.struct(), self.buf, st)
+        if status not in (_lib.JFA_OK, _lib.JFA_ERR_DEVICE):
+            check(status, "jfa_paged_check_error")
+        return flag
+
+    def clear_error(self, cache: PagedKVCache, stream=None) -> None:
+        guard, st = _on(cache.device, stream)
+        with guard:
+            check(_lib.jfa_paged_clear_error(cache.struct(), self.buf, st), "jfa_paged_clear_error")
+
+
+def _ws(cache, ws, where):
+    if ws.buf.numel() < cache.workspace_bytes or ws.buf.device != cache.device:
+        _refuse(where, f"workspace must hold {cache.workspace_bytes} bytes on {cache.device}")
+    return ws.buf
+
+
+def paged_append(cache: PagedKVCache, k, v, ws: PagedWorkspace, cu=None, stream=None) -> None:
+    """Append rows bf16 [T, H_kv, 128] of keys and values (any token and head
+    strides that are multiples of 8).  cu (int32 [batch + 1], device): rows
+    cu[b] .. cu[b + 1] - 1 are sequence b's newest tokens; without it every
+    sequence has T / batch, and idle ones (length 0) are left alone.  The
+    table's lengths already count the new tokens (PageTable.grow)."""
+    where = "paged_append"
+    dev, batch = cache.device, cache.table.batch
+    ka, va = _rows(k, cache.num_kv_heads, dev, where, "k"), _rows(v, cache.num_kv_heads, dev, where, "v")
+    if k.shape[0] != v.shape[0]:
+        _refuse(where, "k and v must hold the same tokens")
+    cup = None if cu is None else _int32(cu, batch + 1, dev, where, "cu")
+    guard, st = _on(dev, stream)
+    with guard:
+        check(_lib.jfa_paged_append(cache.struct(), *ka, *va, cup, k.shape[0], _ws(cache, ws, where), st),
+              "jfa_paged_append")
+
+
+def paged_gather(cache: PagedKVCache, cu, total: int, ws: PagedWorkspace, start=None, k_out=None, v_out=None,
+                 stream=None):
+    """Read rows back: tokens start[b] (from 0 on without start) and following
+    of sequence b into rows cu[b] .. cu[b + 1] - 1 of bf16 [total, H_kv, 128];
+    rows in no range are left as they are (unset in a new output).  Returns (k, v)."""
+    torch = _torch()
+    where = "paged_gather"
+    dev, batch = cache.device, cache.table.batch
+    shape = (total, cache.num_kv_heads, _lib.HEAD_DIM)
+    if total < 0:
+        _refuse(where, "total must not be negative")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if x.shape != shape or x.dtype != torch.bfloat16 or x.device != dev or not x.is_contiguous():
+            _refuse(where, f"{name} must be contiguous bf16 {list(shape)} on {dev}")
+    cup = _int32(cu, batch + 1, dev, where, "cu")
+    stp = None if start is None else _int32(start, batch, dev, where, "start")
+    guard, st = _on(dev, stream)
+    with guard:
+        check(_lib.jfa_paged_gather(cache.struct(), cup, stp, total, k_out, v_out, _ws(cache, ws, where), st),
+              "jfa_paged_gather")
+    return k_out, v_out
+
+
+def paged_attend(cache: PagedKVCache, q, ws: PagedWorkspace, scale=None, window: int = 0, sinks: int = 0,
+                 out=None, lse=None, stream=None):
+    """Attention of each sequence's newest token over its cached tokens, or
+    (window > 0) over the last ``window`` of them and the first ``sinks``.
+
+    q: bf16 [B, H, 128] (heads contiguous, any row stride that is a multiple
+    of 8).  Returns out bf16 [B, H, 128], zeros for an idle sequence; lse (fp32
+    [B, H], if given) gets the natural logarithm of the softmax's sum."""
+    torch = _torch()
+    where = "paged_attend"
+    dev, batch, heads = cache.device, cache.table.batch, cache.num_heads
+    qp, q_row, q_head = _rows(q, heads, dev, where, "q")
+    if q.shape[0] != batch or (q_head != _lib.HEAD_DIM and heads > 1):
+        _refuse(where, f"q must hold {batch} tokens, its heads contiguous")
+    if out is None:
+        out = torch.empty((batch, heads, _lib.HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
+        _refuse(where, f"out must be contiguous bf16 {list(q.shape)} on {dev}")
+    if lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != dev
+                            or not lse.is_contiguous()):
+        _refuse(where, f"lse must be contiguous fp32 [{batch}, {heads}] on {dev}")
+    scale = 1.0 / math.sqrt(_lib.HEAD_DIM) if scale is None else float(scale)
+    if not (scale > 0 and math.isfinite(scale)):
+        _refuse(where, "scale must be positive and finite")
+    guard, st = _on(dev, stream)
+    with guard:
+        check(_lib.jfa_paged_attend(cache.struct(), qp, q_row, scale, window, sinks, _ws(cache, ws, where),
+                                    out, lse, st), "jfa_paged_attend")
+    return out
+
+
+def paged_fork(cache: PagedKVCache, pairs, ws: PagedWorkspace, stream=None) -> None:
+    """For each (parent, child) of pairs (int32 [n, 2], device): the child takes
+    the parent's pages, length and tail.  A child may be no parent, and the
+    child of one pair only (PageTable.fork books this)."""
+    where = "paged_fork"
+    n = pairs.shape[0]
+    if n > cache.table.batch:
+        _refuse(where, f"{n} pairs for {cache.table.batch} sequences")
+    p = _int32(pairs, 2 * n, cache.device, where, "pairs")
+    guard, st = _on(cache.device, stream)
+    with guard:
+        check(_lib.jfa_paged_fork(cache.struct(), p, n, _ws(cache, ws, where), st), "jfa_paged_fork")
+
+
+def paged_move(cache: PagedKVCache, moves, ws: PagedWorkspace, remap=None, stream=None) -> None:
+    """Copy pages (from, to) of moves (int32 [n, 2], device) and, with remap
+    (int32 [n_pages], device), point the table's entries to the new places.
+    No page may be both source and destination, or twice a destination
+    (PageTable.compact books such moves)."""
+    where = "paged_move"
+    n = moves.shape[0]
+    if n > cache.table.n_pages:
+        _refuse(where, f"{n} moves for {cache.table.n_pages} pages")
+    m = _int32(moves, 2 * n, cache.device, where, "moves")
+    r = None if remap is None else _int32(remap, cache.table.n_pages, cache.device, where, "remap")
+    guard, st = _on(cache.device, stream)
+    with guard:
+        check(_lib.jfa_paged_move(cache.struct(), m if n else None, n, r, _ws(cache, ws, where), st),
+              "jfa_paged_move")
+
+
+def paged_decode_step(cache: PagedKVCache, q, k, v, positions, plan: RotaryPlan, ws: PagedWorkspace,
+                      q_weight=None, k_weight=None, eps: float = 1e-6, scale=None, window: int = 0,
+                      sinks: int = 0, out=None, lse=None, stream=None):
+    """One decode step of a layer: norm and rotate the new token's heads,
+    append its key and value, attend.  q bf16 [B, H, 128], k and v bf16
+    [B, H_kv, 128] (slices of one projection's output will do), positions
+    [B]; the table has grown by one token a sequence (PageTable.grow(1)).
+    Three launches.  Returns out bf16 [B, H, 128]."""
+    if q.shape[0] != cache.table.batch:
+        _refuse("paged_decode_step", f"q must hold {cache.table.batch} tokens")
+    q, k = qk_norm_rope(q, k, positions, plan, q_weight, k_weight, eps, stream=stream)
+    paged_append(cache, k, v, ws, stream=stream)
+    return paged_attend(cache, q, ws, scale, window, sinks, out, lse, stream=stream)

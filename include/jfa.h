@@ -69,7 +69,7 @@ typedef enum jfa_status {
 
 /* Device error flag bits (OR-ed into the workspace flag word). */
 #define JFA_DEVERR_NONFINITE_QUANT 0x1u /* a packed scale/zero is inf/nan   */
-#define JFA_DEVERR_BAD_INDEX 0x2u       /* top-k index outside [0, N_q)     */
+#define JFA_DEVERR_BAD_INDEX 0x2u       /* index, page or length out of range */
 #define JFA_DEVERR_TIMEOUT 0x4u         /* a bounded wait gave up           */
 
 typedef struct jfa_geom {
@@ -517,6 +517,131 @@ int jfa_onebit_pack(const jfa_geom* geom, int32_t n_from, int32_t n_to, const ui
 int jfa_onebit_attend(const jfa_geom* geom, const void* pool, const uint16_t* q, float scale,
                       const uint16_t* k_exact, const uint16_t* v_exact, int32_t exact_on_host,
                       void* ws, float* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Head norms and rotary positions, one pass in front of the cache
+ *
+ *   y = x * rsqrt(mean(x^2) + eps) * w          (weight null: y = x)
+ *   (a, b) -> m (a cos p f_i - b sin p f_i,  a sin p f_i + b cos p f_i)
+ * for every query and key head of a token at position p, i < rotary_dim / 2:
+ * (a, b) are channels (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * interleaved; channels from rotary_dim on are not turned (nor scaled by m).
+ * ------------------------------------------------------------------------- */
+typedef struct jfa_rope {
+  int32_t n_tokens;     /* T >= 0                                             */
+  int32_t num_heads;    /* query heads, >= 0                                  */
+  int32_t num_kv_heads; /* key heads, >= 0                                    */
+  int32_t rotary_dim;   /* even, 2..128                                       */
+  int32_t interleaved;  /* pairs (2i, 2i + 1) instead of (i, i + rotary_dim/2) */
+  int32_t positions64;  /* positions are int64 (else int32)                   */
+  float eps;            /* of the norms, >= 0                                 */
+  float amplitude;      /* m                                                  */
+  /* bf16 [T][heads][128]: the 128 channels contiguous, token and head strides
+   * in elements, multiples of 8; pointers 16-byte aligned.  An output may be
+   * its input (same pointer and strides); other overlaps are not allowed. */
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t q_tok, q_head, k_tok, k_head;
+  int64_t qo_tok, qo_head, ko_tok, ko_head;
+  const uint16_t* q_weight; /* bf16 [128], or null: no norm                   */
+  const uint16_t* k_weight;
+  const void* positions;    /* [T], device                                    */
+  const uint64_t* freq;     /* [rotary_dim / 2], device: f_i / (2 pi) in
+                             * units of 2^-64 turns                           */
+} jfa_rope;
+
+/* fp32 arithmetic, one rounding.  One launch.  Stream-ordered. */
+int jfa_qk_norm_rope(const jfa_rope* rope, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged 4-bit cache
+ *
+ * One layer's K4V4 cache in pages of 64 tokens.  A page holds one record
+ * (jfa_unpack_record decodes it) per KV head.  table[b] lists sequence b's
+ * pages in order; the newest 1..64 tokens of a sequence are exact, in its
+ * tail, so N_q(n) = 64 * ((n - 1) / 64) tokens of n are in pages.  A page is
+ * written once, when its 64 tokens are complete: sequences may share it.
+ * The table and the lengths are read on the device, so a captured graph
+ * follows them as they grow; several layers may share one table.
+ *
+ * Entries of the table that a call needs and that lie outside [0, n_pages),
+ * lengths outside [0, 64 max_pages + 64], row ranges outside their tensors,
+ * bad pairs, and moves outside the pool or against their remap set
+ * JFA_DEVERR_BAD_INDEX in the workspace; what they name is skipped.  A
+ * non-finite scale or zero point that is packed sets
+ * JFA_DEVERR_NONFINITE_QUANT.
+ * ------------------------------------------------------------------------- */
+#define JFA_PAGE_RECORD_BYTES 9728 /* a page of one KV head */
+
+typedef struct jfa_paged {
+  int32_t batch;        /* sequences (rows of the table), 1..JFA_MAX_BATCH     */
+  int32_t num_heads;    /* H % H_kv == 0, H / H_kv <= 8                        */
+  int32_t num_kv_heads; /* H_kv                                                */
+  int32_t n_pages;      /* pages of the pool, >= 1                             */
+  int32_t max_pages;    /* entries of a table row, >= 1                        */
+  int32_t reserved;     /* 0                                                   */
+  void* pages;          /* [n_pages][H_kv][JFA_PAGE_RECORD_BYTES]              */
+  uint16_t* tail_k;     /* bf16 [batch][H_kv][64][128]; 16-byte chunk c of     */
+  uint16_t* tail_v;     /*   slot t at chunk position c ^ (t & 7) of its row   */
+  int32_t* table;       /* [batch][max_pages]                                  */
+  int32_t* seq_lens;    /* [batch]; 0: the row is idle                         */
+} jfa_paged;            /* device pointers, 16-byte aligned (table, seq_lens: 4) */
+
+/* Workspace of the paged calls (256-byte aligned; zero before its first
+ * call).  Calls that may run at the same time need one each. */
+int jfa_paged_workspace_bytes(const jfa_paged* cache, size_t* bytes);
+
+/* Append rows.  Row range [cu[b], cu[b + 1]) of k_new / v_new (bf16
+ * [n_total][H_kv][128], channels contiguous, strides in elements, multiples
+ * of 8) holds sequence b's newest tokens; cu null: n_total / batch rows each
+ * (n_total a multiple of batch), sequences of length 0 left alone.  seq_lens
+ * are the lengths WITH the new tokens.  Groups that are complete are
+ * quantized (jfa_pack_kv's rule) into the table's pages, the rest becomes the
+ * tail.  cu: int32 [batch + 1], device.  One launch.  Stream-ordered. */
+int jfa_paged_append(const jfa_paged* cache, const uint16_t* k_new, int64_t k_tok, int64_t k_head,
+                     const uint16_t* v_new, int64_t v_tok, int64_t v_head, const int32_t* cu,
+                     int32_t n_total, void* ws, void* stream);
+
+/* Read rows back as bf16 (dequantized where packed, else the exact rows):
+ * tokens start[b] .. start[b] + cu[b + 1] - cu[b] - 1 of sequence b (start
+ * null: from 0) into rows [cu[b], cu[b + 1]) of k_out / v_out [n_total][H_kv]
+ * [128]; other rows are left as they are.  cu int32 [batch + 1], start int32
+ * [batch], device.  One launch.  Stream-ordered. */
+int jfa_paged_gather(const jfa_paged* cache, const int32_t* cu, const int32_t* start,
+                     int32_t n_total, uint16_t* k_out, uint16_t* v_out, void* ws, void* stream);
+
+/* Attention of one query token per sequence (the newest, at seq_lens[b] - 1)
+ * over its cache: softmax over the visible tokens of scale q_h . k_t, applied
+ * to v_t.  Visible: every token, or with window > 0 those with
+ * t >= seq_lens[b] - window or t < sinks.  q: bf16 [batch][H][128], rows
+ * q_row elements apart (a multiple of 8, heads contiguous).  out: bf16
+ * [batch][H][128] contiguous, zeros for an idle sequence; lse (may be null):
+ * fp32 [batch][H], the natural logarithm of the sum of exp(scale q.k), -inf
+ * for an idle one.  One launch.  Stream-ordered. */
+int jfa_paged_attend(const jfa_paged* cache, const uint16_t* q, int64_t q_row, float scale,
+                     int32_t window, int32_t sinks, void* ws, uint16_t* out, float* lse,
+                     void* stream);
+
+/* Forks: for each of the n pairs (parent, child) (int32 [n][2], device) the
+ * child takes the parent's table row, length and tail; the packed pages are
+ * shared.  No child may be a parent or a child of another pair.  Of layers
+ * with one table, the call is made for each.  n <= batch.  One launch. */
+int jfa_paged_fork(const jfa_paged* cache, const int32_t* pairs, int32_t n, void* ws, void* stream);
+
+/* Copy pages: for each of the n moves (from, to) (int32 [n][2], device); no
+ * page may be both a source and a destination, nor twice a destination.  With
+ * remap (int32 [n_pages], device; may be null) the entries of the table that
+ * hold packed tokens follow: e becomes remap[e].  Then the moves have to be
+ * those pages of remap that change place, onto pages that do not.  Of layers
+ * with one table, one call carries remap.  One launch. */
+int jfa_paged_move(const jfa_paged* cache, const int32_t* moves, int32_t n, const int32_t* remap,
+                   void* ws, void* stream);
+
+/* The workspace's error flag, as jfa_check_error and jfa_clear_error. */
+int jfa_paged_check_error(const jfa_paged* cache, void* ws, void* stream, uint32_t* flag_out);
+int jfa_paged_clear_error(const jfa_paged* cache, void* ws, void* stream);
 
 /* Number of warps jfa_decode_scores splits the quantized groups over on the
  * current device (0 on a bad geometry or when no group is quantized).  Warp w

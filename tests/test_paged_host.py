@@ -1,0 +1,319 @@
+"""CPU checks of the paged cache's host side: the page book-keeping, the rotary
+frequencies, the workspace's size, and the refusals of every entry point before
+any launch."""
+import math
+import random
+
+import pytest
+import torch
+
+import bit_kv_cache_jfa_b200 as jfa
+from bit_kv_cache_jfa_b200 import JfaError, _lib
+
+BAD = _lib.JFA_ERR_INVALID_ARG
+UNSUPPORTED = _lib.JFA_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from bit_kv_cache_jfa_b200 import build
+    build.build()
+
+
+def _split(n):
+    return 0 if n <= 0 else (n - 1) // 64
+
+
+def _check_book(t):
+    """Device copies as the host's book; every page counted once per row that lists it."""
+    assert t.seq_lens.tolist() == t.lens
+    count = [0] * t.n_pages
+    for b, row in enumerate(t.rows):
+        assert len(row) == _split(t.lens[b])
+        for p in row:
+            count[p] += 1
+    assert count == t._refs
+    assert sorted(t._free) == [p for p in range(t.n_pages) if count[p] == 0]
+
+
+def _check_table(t):
+    for b, row in enumerate(t.rows):
+        assert t.table[b, :len(row)].tolist() == row
+
+
+def test_grow_gives_pages_when_groups_complete():
+    t = jfa.PageTable(3, 8, 4, device="cpu")
+    cu = t.grow([64, 0, 65])
+    assert cu.tolist() == [0, 64, 64, 129] and cu.dtype == torch.int32
+    assert t.rows == [[], [], [0]] and t.lens == [64, 0, 65]
+    assert t.grow(1) is None                         # the idle row stays idle
+    assert t.lens == [65, 0, 66] and t.rows == [[1], [], [0]]
+    _check_book(t)
+    _check_table(t)
+    t.grow([130, 1, 0])
+    assert t.lens == [195, 1, 66] and t.rows[0] == [1, 2, 3]
+    _check_book(t)
+    _check_table(t)
+
+
+def test_grow_refuses_without_changing_anything():
+    t = jfa.PageTable(2, 3, 2, device="cpu")
+    t.grow([100, 30])
+    before = (list(t.lens), [list(r) for r in t.rows], t.table.clone())
+    for counts in ([100, 0], [0, 200], [-1, 0], [1], [60, 100]):
+        with pytest.raises(JfaError) as e:
+            t.grow(counts)
+        assert e.value.status == BAD
+        assert (t.lens, t.rows) == before[:2] and torch.equal(t.table, before[2])
+        _check_book(t)
+
+
+def test_fork_shares_and_free_counts():
+    t = jfa.PageTable(4, 10, 4, device="cpu")
+    t.grow([200, 70, 0, 0])
+    pairs = t.fork([(0, 2), (0, 1)])
+    assert pairs.tolist() == [[0, 2], [0, 1]] and pairs.dtype == torch.int32
+    assert t.rows[1] == t.rows[2] == t.rows[0] and t.lens == [200, 200, 200, 0]
+    assert t.free_pages == 7                         # row 1's own page is free again
+    t.free([0])
+    assert t.free_pages == 7 and t.lens[0] == 0
+    t.free([1, 2])
+    assert t.free_pages == 10
+    for bad in ([(1, 1)], [(0, 1), (1, 2)], [(0, 1), (2, 1)], [(0, 4)], [(-1, 0)]):
+        with pytest.raises(JfaError):
+            t.fork(bad)
+    with pytest.raises(JfaError):
+        t.free([4])
+
+
+def test_compact_moves_pages_in_use_to_the_front():
+    t = jfa.PageTable(4, 40, 8, device="cpu")
+    t.grow([300, 200, 500, 0])
+    t.fork([(2, 3)])
+    t.free([0, 1])
+    rows = [list(r) for r in t.rows]
+    moves, remap = t.compact()
+    n_used = 7
+    assert sorted({p for r in t.rows for p in r}) == list(range(n_used))
+    remap = remap.tolist()
+    assert [[remap[p] for p in r] for r in rows] == t.rows
+    src, dst = zip(*moves.tolist())
+    assert not set(src) & set(dst) and len(set(src)) == len(src) and len(set(dst)) == len(dst)
+    for a, b in moves.tolist():
+        assert remap[a] == b and remap[b] == b
+    assert all(remap[p] == p for p in range(40) if p not in src)
+    assert t.seq_lens.tolist() == t.lens == [0, 0, 500, 500]
+    moves, _ = t.compact()
+    assert moves.shape == (0, 2)
+
+
+def test_random_book_keeping():
+    rng = random.Random(5)
+    t = jfa.PageTable(6, 60, 12, device="cpu")
+    for _ in range(300):
+        op = rng.randrange(4)
+        try:
+            if op == 0:
+                t.grow([rng.choice([0, 1, 5, 64, 130]) for _ in range(6)])
+            elif op == 1:
+                t.grow(1)
+            elif op == 2:
+                a, b = rng.sample(range(6), 2)
+                t.fork([(a, b)])
+                # what paged_fork does on the device
+                t.table[b], t.seq_lens[b] = t.table[a].clone(), t.lens[b]
+            else:
+                t.free([rng.randrange(6)])
+        except JfaError:
+            pass
+        _check_book(t)
+        _check_table(t)
+
+
+@pytest.mark.parametrize("scaling,kw", [
+    ("none", {}), ("linear", dict(factor=4.0)),
+    ("llama3", dict(factor=8.0, low_freq_factor=1.0, high_freq_factor=4.0, original=8192)),
+    ("yarn", dict(factor=16.0, original=16384))])
+@pytest.mark.parametrize("rotary", [2, 6, 64, 128])
+def test_rotary_frequencies(scaling, kw, rotary):
+    base = 500000.0
+    plan = jfa.RotaryPlan(rotary, base=base, scaling=scaling, device="cpu", **kw)
+    for i, (f, turn) in enumerate(zip(plan.frequencies, plan.freq.tolist())):
+        w = base ** (-2 * i / rotary)
+        if scaling == "linear":
+            want = w / 4
+        elif scaling == "llama3":
+            length = 2 * math.pi / w
+            if length < 8192 / 4:
+                want = w
+            elif length > 8192:
+                want = w / 8
+            else:
+                u = (8192 / length - 1) / 3
+                want = (1 - u) * w / 8 + u * w
+        elif scaling == "yarn":
+            lo, hi = (rotary * math.log(16384 / (b * 2 * math.pi)) / (2 * math.log(base)) for b in (32, 1))
+            lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rotary - 1)
+            u = min(max((i - lo) / max(hi - lo, 1e-3), 0), 1)
+            want = u * w / 16 + (1 - u) * w
+        else:
+            want = w
+        assert math.isclose(f, want, rel_tol=1e-13)
+        # a whole number of units of 2 pi 2^-64: half a unit off, 1e-12 of the slowest frequency here
+        assert math.isclose((turn % 2**64) / 2**64 * 2 * math.pi, f, rel_tol=1e-13, abs_tol=math.pi * 2.0**-64)
+    assert plan.freq.shape == (rotary // 2,)
+    assert math.isclose(plan.amplitude, 0.1 * math.log(16) + 1 if scaling == "yarn" else 1.0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rotary_dim=0), dict(rotary_dim=130), dict(rotary_dim=7), dict(base=1.0), dict(factor=0.0),
+    dict(scaling="other"), dict(scaling="llama3"), dict(scaling="yarn"),
+    dict(scaling="llama3", original=8192, low_freq_factor=4.0),
+    dict(scaling="yarn", original=8192, beta_slow=40.0), dict(amplitude=math.inf)])
+def test_rotary_plan_refusals(kw):
+    with pytest.raises(JfaError) as e:
+        jfa.RotaryPlan(device="cpu", **kw)
+    assert e.value.status == BAD
+
+
+def _paged(**kw):
+    d = dict(batch=2, num_heads=8, num_kv_heads=2, n_pages=10, max_pages=5, reserved=0, pages=256,
+             tail_k=256, tail_v=256, table=256, seq_lens=256)
+    d.update(kw)
+    return _lib.Paged(*d.values())
+
+
+def test_workspace_bytes():
+    n = _lib.jfa_paged_workspace_bytes(_paged())
+    part = 8 * 132 * 4                               # a partial of 8 heads
+    assert n == 256 + 256 + 192 * (2 + 16) * part
+    assert _lib.jfa_paged_workspace_bytes(_paged(batch=256, num_kv_heads=8)) == n + 256 * 8 * 4 - 256
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(batch=0), BAD), (dict(batch=257), BAD), (dict(num_heads=9), BAD), (dict(num_kv_heads=0), BAD),
+    (dict(num_heads=18, num_kv_heads=2), BAD), (dict(n_pages=0), BAD), (dict(max_pages=0), BAD),
+    (dict(max_pages=1 << 26), UNSUPPORTED), (dict(num_heads=1 << 17, num_kv_heads=1 << 16), UNSUPPORTED),
+    (dict(batch=256, num_heads=256, num_kv_heads=256, max_pages=1 << 16), UNSUPPORTED)])
+def test_bad_sizes_refused(bad, status):
+    c = _paged(**bad)
+    with pytest.raises(JfaError) as e:
+        _lib.jfa_paged_workspace_bytes(c)
+    assert e.value.status == status
+    assert _lib.jfa_paged_append(c, 256, 8, 8, 256, 8, 8, 256, 2, 256) == status
+    assert _lib.jfa_paged_gather(c, 256, None, 2, 256, 256, 256) == status
+    assert _lib.jfa_paged_attend(c, 256, 1024, 0.1, 0, 0, 256, 256) == status
+    assert _lib.jfa_paged_fork(c, 256, 1, 256) == status
+    assert _lib.jfa_paged_move(c, 256, 1, 256, 256) == status
+
+
+@pytest.mark.parametrize("bad", [dict(pages=0), dict(pages=264), dict(tail_k=0), dict(tail_v=8), dict(table=0),
+                                 dict(table=258), dict(seq_lens=0)])
+def test_bad_buffers_refused(bad):
+    c = _paged(**bad)
+    assert _lib.jfa_paged_append(c, 256, 8, 8, 256, 8, 8, 256, 2, 256) == BAD
+    assert _lib.jfa_paged_attend(c, 256, 1024, 0.1, 0, 0, 256, 256) == BAD
+    assert _lib.jfa_paged_move(c, 256, 1, None, 256) == BAD
+
+
+def test_bad_arguments_refused_before_launch():
+    c = _paged()
+    # append: count, uniform split, pointers, strides, workspace
+    assert _lib.jfa_paged_append(c, 256, 8, 8, 256, 8, 8, 256, -1, 256) == BAD
+    assert _lib.jfa_paged_append(c, 256, 8, 8, 256, 8, 8, None, 3, 256) == BAD
+    assert _lib.jfa_paged_append(c, None, 8, 8, 256, 8, 8, 256, 2, 256) == BAD
+    assert _lib.jfa_paged_append(c, 256, 12, 8, 256, 8, 8, 256, 2, 256) == BAD
+    assert _lib.jfa_paged_append(c, 256, 8, 8, 260, 8, 8, 256, 2, 256) == BAD
+    assert _lib.jfa_paged_append(c, 256, 8, 8, 256, 8, 8, 256, 2, 128) == BAD
+    assert _lib.jfa_paged_append(c, 256, 8, 8, 256, 8, 8, 256, 2, None) == BAD
+    assert _lib.jfa_paged_append(c, None, 8, 8, None, 8, 8, None, 0, 256) == 0     # nothing to do
+    # gather
+    assert _lib.jfa_paged_gather(c, None, None, 2, 256, 256, 256) == BAD
+    assert _lib.jfa_paged_gather(c, 256, 258, 2, 256, 256, 256) == BAD
+    assert _lib.jfa_paged_gather(c, 256, None, -2, 256, 256, 256) == BAD
+    assert _lib.jfa_paged_gather(c, 256, None, 2, 256, 264, 256) == BAD
+    assert _lib.jfa_paged_gather(c, 256, None, 0, None, None, 256) == 0
+    # attend
+    for args in ((None, 1024, 0.1, 0, 0, 256, 256), (256, 1028, 0.1, 0, 0, 256, 256),
+                 (256, 1024, 0.0, 0, 0, 256, 256), (256, 1024, math.nan, 0, 0, 256, 256),
+                 (256, 1024, 0.1, -1, 0, 256, 256), (256, 1024, 0.1, 0, -1, 256, 256),
+                 (256, 1024, 0.1, 0, 0, 256, None), (256, 1024, 0.1, 0, 0, 64, 256)):
+        assert _lib.jfa_paged_attend(c, *args) == BAD
+    assert _lib.jfa_paged_attend(c, 256, 1024, 0.1, 0, 0, 256, 256, 258) == BAD    # lse
+    # fork and move
+    assert _lib.jfa_paged_fork(c, 256, 3, 256) == BAD
+    assert _lib.jfa_paged_fork(c, None, 1, 256) == BAD
+    assert _lib.jfa_paged_fork(c, None, 0, 256) == 0
+    assert _lib.jfa_paged_move(c, 256, 11, None, 256) == BAD
+    assert _lib.jfa_paged_move(c, None, 1, None, 256) == BAD
+    assert _lib.jfa_paged_move(c, None, 0, None, 256) == 0
+
+
+def _rope(**kw):
+    d = dict(n_tokens=3, num_heads=4, num_kv_heads=2, rotary_dim=128, interleaved=0, positions64=0, eps=1e-6,
+             amplitude=1.0, q=256, k=256, q_out=256, k_out=256, q_tok=512, q_head=128, k_tok=256, k_head=128,
+             qo_tok=512, qo_head=128, ko_tok=256, ko_head=128, q_weight=0, k_weight=0, positions=256, freq=256)
+    d.update(kw)
+    return _lib.Rope(*d.values())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_tokens=-1), dict(num_heads=-1), dict(rotary_dim=0), dict(rotary_dim=129), dict(rotary_dim=130),
+    dict(eps=-1.0), dict(eps=math.nan), dict(amplitude=math.nan), dict(q=0), dict(q=264), dict(k_out=0),
+    dict(q_tok=513), dict(k_head=4), dict(ko_tok=130), dict(q_weight=264), dict(positions=0),
+    dict(positions=258), dict(positions=260, positions64=1), dict(freq=0), dict(freq=260)])
+def test_rope_refusals(bad):
+    assert _lib.jfa_qk_norm_rope(_rope(**bad)) == BAD
+
+
+def test_rope_nothing_to_do():
+    assert _lib.jfa_qk_norm_rope(_rope(n_tokens=0, q=0, k=0, positions=0)) == 0
+    assert _lib.jfa_qk_norm_rope(_rope(num_heads=0, num_kv_heads=0, q=0, k=0)) == 0
+    assert _lib.jfa_qk_norm_rope(_rope(num_heads=(1 << 20) + 1)) == UNSUPPORTED
+
+
+def test_python_layer_refusals():
+    for args in ((0, 4, 4), (257, 4, 4), (2, 0, 4), (2, 4, 0)):
+        with pytest.raises(JfaError):
+            jfa.PageTable(*args, device="cpu")
+    t = jfa.PageTable(2, 4, 4, device="cpu")
+    with pytest.raises(JfaError):
+        jfa.PagedKVCache(t, 9, 2)
+    cache = jfa.PagedKVCache(t, 8, 2)
+    ws = jfa.PagedWorkspace(cache)
+    rows = torch.zeros(2, 2, 128, dtype=torch.bfloat16)
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    cu = torch.zeros(3, dtype=torch.int32)
+    plan = jfa.RotaryPlan(device="cpu")
+    refused = [
+        lambda: jfa.paged_append(cache, rows.float(), rows, ws),
+        lambda: jfa.paged_append(cache, rows[:, :1], rows, ws),
+        lambda: jfa.paged_append(cache, rows, rows[:1], ws),
+        lambda: jfa.paged_append(cache, rows, rows, ws, cu.long()),
+        lambda: jfa.paged_append(cache, rows, rows, ws, cu[:2]),
+        lambda: jfa.paged_append(cache, rows.transpose(1, 2).contiguous().transpose(1, 2), rows, ws),
+        lambda: jfa.paged_gather(cache, cu, -1, ws),
+        lambda: jfa.paged_gather(cache, cu, 2, ws, k_out=rows[:1]),
+        lambda: jfa.paged_gather(cache, cu, 2, ws, start=cu),
+        lambda: jfa.paged_attend(cache, q[:1], ws),
+        lambda: jfa.paged_attend(cache, q[:, :4], ws),
+        lambda: jfa.paged_attend(cache, q.transpose(0, 1).contiguous().transpose(0, 1), ws),
+        lambda: jfa.paged_attend(cache, q, ws, scale=-1.0),
+        lambda: jfa.paged_attend(cache, q, ws, scale=math.inf),
+        lambda: jfa.paged_attend(cache, q, ws, out=q.float()),
+        lambda: jfa.paged_attend(cache, q, ws, lse=torch.zeros(2, 4)),
+        lambda: jfa.paged_fork(cache, torch.zeros(3, 2, dtype=torch.int32), ws),
+        lambda: jfa.paged_fork(cache, torch.zeros(1, 2), ws),
+        lambda: jfa.paged_move(cache, torch.zeros(5, 2, dtype=torch.int32), ws),
+        lambda: jfa.paged_move(cache, torch.zeros(1, 2, dtype=torch.int32), ws, cu),
+        lambda: jfa.qk_norm_rope(q, rows[:1], cu[:2], plan),
+        lambda: jfa.qk_norm_rope(q, rows, cu, plan),
+        lambda: jfa.qk_norm_rope(q, rows, cu[:2].float(), plan),
+        lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, q_weight=torch.zeros(64, dtype=torch.bfloat16)),
+        lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, q_out=rows),
+        lambda: jfa.paged_decode_step(cache, q[:1], rows[:1], rows[:1], cu[:1], plan, ws),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(JfaError) as e:
+            call()
+        assert e.value.status == BAD, i
