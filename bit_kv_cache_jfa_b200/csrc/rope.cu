@@ -14,12 +14,14 @@
 
 namespace jfa {
 
-constexpr int kRpThreads = 256;
-constexpr int kRpRows = kRpThreads / 16;  // heads of one pass: 16 lanes x 8 channels each
+constexpr int kRpWarps = 4;
+constexpr int kRpRows = 8;  // heads of a unit
+
+enum : int { kRpHalf = 0, kRpInter = 1, kRpHalfOdd = 2 };
 
 struct RopeParams {
   jfa_rope r;
-  int half_shfl;  // the partner channels are a whole chunk of another lane
+  uint32_t units, slices;  // units = tokens * slices, slices of kRpRows heads
 };
 
 __device__ __forceinline__ void unpack8(uint4 w, float* x) {
@@ -30,118 +32,172 @@ __device__ __forceinline__ void unpack8(uint4 w, float* x) {
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    o[i] = *reinterpret_cast<uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
 
-// One CTA per token.  Each half warp takes a head: a lane holds 8 consecutive
-// channels (16-byte loads and stores), its cos and sin, computed once per
-// token by the first r/2 threads, stay in registers over the heads.  The
-// partner of a channel in the half layout is r/2 away: 8-channel chunks come
-// by shuffles when r/2 is a multiple of 8, else element by element from the
-// row itself (in the first cache level by then), before any lane stores.
-// HBM-bound from a few hundred tokens on: 512 B per head and token.
-template <bool INTER>
-__global__ void __launch_bounds__(kRpThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 cs_s[kD / 2];
-  const int tid = threadIdx.x, l = tid & 15, hw = tid >> 4;
-  const int64_t t = blockIdx.x;
-  const int r = p.r.rotary_dim, h2 = r >> 1;
+// A warp per unit: eight heads of one token, four at a time, 8 lanes a head.
+// All its rows are requested first, the sines and cosines (two pairs a lane)
+// are formed meanwhile and shared through 512 bytes of shared memory.  A lane
+// holds two 16-byte chunks of its head:
+//   kRpHalf (r a multiple of 16): the chunks of channels i and i + r/2, so
+//     the pairs are its own, and 8 pairs' cos and sin serve 16 channels;
+//   kRpInter: chunks l and l + 8, pairs within them;
+//   kRpHalfOdd: chunks l and l + 8; the partners come through shared memory
+//     (fp32, a 9-float pitch a chunk against bank conflicts).
+// HBM-bound when there are many tokens: 512 B a head.  A token's sines are
+// formed again by each of its warps (about 100 of a unit's 300 instructions):
+// that costs less than the wait of a whole block for one token's.
+template <int MODE>
+__global__ void __launch_bounds__(32 * kRpWarps) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float2 cs_s[kRpWarps][kD / 2];
+  __shared__ float ex_s[MODE == kRpHalfOdd ? kRpWarps : 1][MODE == kRpHalfOdd ? 4 * 145 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane >> 3, l = lane & 7;
+  const uint32_t u = blockIdx.x * kRpWarps + warp;
   pdl_wait();
-  if (tid < h2) {
-    const int64_t pos = p.r.positions64 ? static_cast<const int64_t*>(p.r.positions)[t]
-                                : (int64_t)static_cast<const int32_t*>(p.r.positions)[t];
-    const uint64_t turn = (uint64_t)pos * p.r.freq[tid];
-    float sn, cs;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
-    cs_s[tid] = make_float2(cs * p.r.amplitude, sn * p.r.amplitude);
-  }
-  const int rows = p.r.num_heads + p.r.num_kv_heads;
-  const int c0 = 8 * l;
-  const bool turned = c0 < r;  // some of the lane's channels rotate
-  __syncthreads();
-  // this lane's cos and signed sin (the partner's weight) per channel
-  float cs[8], sn[8];
-  int pc[8];  // partner channel
+  if (u >= p.units) return;
+  const uint32_t tok = u / p.slices;
+  const int64_t t = tok;
+  const int r = p.r.rotary_dim, h2 = r >> 1, nq = p.r.num_heads, rows = nq + p.r.num_kv_heads;
+  const int row0 = (int)(u - tok * p.slices) * kRpRows + sub;
+  const int hc = h2 >> 3;  // kRpHalf: chunks of half the rotary channels
+  const int ca = MODE != kRpHalf || l < hc ? l : 2 * l;  // past them: 2 hc + 2 (l - hc)
+  const int cb = MODE != kRpHalf ? l + 8 : (l < hc ? l + hc : 2 * l + 1);
+  uint4 raw[2][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = c0 + i;
-    const bool on = c < r;
-    const bool first = INTER ? (i & 1) == 0 : c < h2;
-    const int k = INTER ? c >> 1 : (first ? c : c - h2);
-    const float2 v = on ? cs_s[k] : make_float2(1.f, 0.f);
-    cs[i] = v.x;
-    sn[i] = first ? -v.y : v.y;
-    pc[i] = on ? (INTER ? c ^ 1 : (first ? c + h2 : c - h2)) : c;
-  }
-  const int psrc = (tid & 16) + (pc[0] >> 3);  // the lane that holds the partner chunk
-  const uint16_t* held = nullptr;
-  float wa[8], wb[8];
-  for (int row = hw; row < rows; row += kRpRows) {
-    const bool is_q = row < p.r.num_heads;
-    const int head = is_q ? row : row - p.r.num_heads;
-    const uint16_t* x = is_q ? p.r.q + t * p.r.q_tok + head * p.r.q_head : p.r.k + t * p.r.k_tok + head * p.r.k_head;
-    uint16_t* y = is_q ? p.r.q_out + t * p.r.qo_tok + head * p.r.qo_head
-                       : p.r.k_out + t * p.r.ko_tok + head * p.r.ko_head;
-    const uint16_t* w = is_q ? p.r.q_weight : p.r.k_weight;
-    const unsigned mask = 0xFFFFu << (tid & 16);
-    const uint4 raw = *reinterpret_cast<const uint4*>(x + c0);
-    float a[8], b[8];
-    unpack8(raw, a);
-    // raw partner channels
-    if (INTER) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = a[i ^ 1];
-    } else if (p.half_shfl) {
-      uint4 pw;
-      pw.x = __shfl_sync(mask, raw.x, psrc);
-      pw.y = __shfl_sync(mask, raw.y, psrc);
-      pw.z = __shfl_sync(mask, raw.z, psrc);
-      pw.w = __shfl_sync(mask, raw.w, psrc);
-      unpack8(pw, b);
+  for (int i = 0; i < 2; ++i) {
+    const int row = row0 + 4 * i;
+    if (row < rows) {
+      const uint16_t* x = row < nq ? p.r.q + t * p.r.q_tok + row * p.r.q_head
+                                   : p.r.k + t * p.r.k_tok + (row - nq) * p.r.k_head;
+      raw[i][0] = *reinterpret_cast<const uint4*>(x + 8 * ca);
+      raw[i][1] = *reinterpret_cast<const uint4*>(x + 8 * cb);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = turned ? __uint_as_float((uint32_t)x[pc[i]] << 16) : 0.f;
-      __syncwarp(mask);  // every lane has read before any stores in place
+      raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
     }
-    if (w) {
+  }
+  {
+    const int64_t pos = p.r.positions64 ? static_cast<const int64_t*>(p.r.positions)[t]
+                                        : (int64_t) static_cast<const int32_t*>(p.r.positions)[t];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = lane + 32 * i;
+      if (k < h2) {
+        const uint64_t turn = (uint64_t)pos * p.r.freq[k];
+        float sn, cs;
+        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
+        cs_s[warp][k] = make_float2(cs * p.r.amplitude, sn * p.r.amplitude);
+      }
+    }
+    __syncwarp();
+  }
+  constexpr int NC = MODE == kRpHalfOdd ? 16 : 8;
+  float cs[NC], sn[NC];  // of the lane's pairs; kRpHalfOdd: of its channels, sn with the partner's sign
+  int pc[MODE == kRpHalfOdd ? 16 : 1];  // kRpHalfOdd: the partner's place, -1 where a channel passes through
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    float2 v = make_float2(1.f, 0.f);
+    if (MODE == kRpHalf) {
+      if (l < hc) v = cs_s[warp][8 * l + j];
+    } else if (MODE == kRpInter) {
+      const int k = (j < 4 ? 4 * l : 4 * l + 28) + j;
+      if (k < h2) v = cs_s[warp][k];
+    } else {
+      const int c = 8 * l + (j < 8 ? j : j + 56), q = c < h2 ? c + h2 : c - h2;
+      if (c < r) {
+        v = cs_s[warp][min(c, q)];
+        if (c < h2) v.y = -v.y;
+      }
+      pc[MODE == kRpHalfOdd ? j : 0] = c < r ? (q >> 3) * 9 + (q & 7) : -1;
+    }
+    cs[j] = v.x;
+    sn[j] = v.y;
+  }
+  uint4 wr[2];
+  const uint16_t* held = nullptr;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = row0 + 4 * i;
+    const bool is_q = row < nq;
+    const uint16_t* w = is_q ? p.r.q_weight : p.r.k_weight;
+    float x[16], y[16];
+    unpack8(raw[i][0], x);
+    unpack8(raw[i][1], x + 8);
+    if (p.r.q_weight || p.r.k_weight) {
       float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss);
+      for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      const float rs = rsqrtf(ss * (1.f / kD) + p.r.eps);
-      if (w != held) {  // the weights stay over the query heads, then over the key heads
-        held = w;
-        unpack8(*reinterpret_cast<const uint4*>(w + c0), wa);
+      for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      if (w) {
+        const float rs = rsqrtf(ss * (1.f / kD) + p.r.eps);
+        if (w != held) {  // the weights stay over the query heads, then over the key heads
+          held = w;
+          wr[0] = *reinterpret_cast<const uint4*>(w + 8 * ca);
+          wr[1] = *reinterpret_cast<const uint4*>(w + 8 * cb);
+        }
+        float wf[16];
+        unpack8(wr[0], wf);
+        unpack8(wr[1], wf + 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wb[i] = __uint_as_float((uint32_t)w[pc[i]] << 16);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= rs * wa[i];
-        b[i] *= rs * wb[i];
+        for (int j = 0; j < 16; ++j) x[j] *= rs * wf[j];
       }
     }
+    // a channel that passes through is taken as it is, infinite ones too
+    if (MODE == kRpHalf) {
+      const bool on = l < hc;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c0 + i >= r) b[i] = 0.f;  // a channel that passes through, infinite ones too
-    uint32_t o[4];
+      for (int j = 0; j < 8; ++j) {
+        y[j] = on ? fmaf(x[j], cs[j], -x[8 + j] * sn[j]) : x[j];
+        y[8 + j] = on ? fmaf(x[8 + j], cs[j], x[j] * sn[j]) : x[8 + j];
+      }
+    } else if (MODE == kRpInter) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float y0 = fmaf(a[2 * i], cs[2 * i], b[2 * i] * sn[2 * i]);
-      const float y1 = fmaf(a[2 * i + 1], cs[2 * i + 1], b[2 * i + 1] * sn[2 * i + 1]);
-      __nv_bfloat162 v = __floats2bfloat162_rn(y0, y1);
-      o[i] = *reinterpret_cast<uint32_t*>(&v);
+      for (int j = 0; j < 8; ++j) {
+        const bool on = (j < 4 ? 4 * l : 4 * l + 28) + j < h2;
+        y[2 * j] = on ? fmaf(x[2 * j], cs[j], -x[2 * j + 1] * sn[j]) : x[2 * j];
+        y[2 * j + 1] = on ? fmaf(x[2 * j + 1], cs[j], x[2 * j] * sn[j]) : x[2 * j + 1];
+      }
+    } else {
+      float* e = ex_s[MODE == kRpHalfOdd ? warp : 0] + sub * 145;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) e[9 * (j < 8 ? l : l + 8) + (j & 7)] = x[j];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int q = pc[MODE == kRpHalfOdd ? j : 0];
+        y[j] = q >= 0 ? fmaf(x[j], cs[j & (NC - 1)], e[max(q, 0)] * sn[j & (NC - 1)]) : x[j];
+      }
+      __syncwarp();
     }
-    *reinterpret_cast<uint4*>(y + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (row < rows) {
+      uint16_t* o = is_q ? p.r.q_out + t * p.r.qo_tok + row * p.r.qo_head
+                         : p.r.k_out + t * p.r.ko_tok + (row - nq) * p.r.ko_head;
+      *reinterpret_cast<uint4*>(o + 8 * ca) = pack8(y);
+      *reinterpret_cast<uint4*>(o + 8 * cb) = pack8(y + 8);
+    }
   }
 }
 
 int launch_qk_norm_rope(const jfa_rope& r, cudaStream_t st) {
   RopeParams p;
   p.r = r;
-  p.half_shfl = r.rotary_dim % 16 == 0;
-  const dim3 grid((unsigned)r.n_tokens), block(kRpThreads);
-  const cudaError_t e = r.interleaved ? launch_pdl(qk_norm_rope_kernel<true>, grid, block, 0, st, p)
-                                      : launch_pdl(qk_norm_rope_kernel<false>, grid, block, 0, st, p);
+  const long long slices = ((long long)r.num_heads + r.num_kv_heads + kRpRows - 1) / kRpRows;
+  const long long units = slices * r.n_tokens;
+  if (units > 0x7FFFFFFFll) return JFA_ERR_UNSUPPORTED;
+  p.slices = (uint32_t)slices;
+  p.units = (uint32_t)units;
+  const dim3 grid((unsigned)((units + kRpWarps - 1) / kRpWarps)), block(32 * kRpWarps);
+  cudaError_t e;
+  if (r.interleaved) e = launch_pdl(qk_norm_rope_kernel<kRpInter>, grid, block, 0, st, p);
+  else if (r.rotary_dim % 16 == 0) e = launch_pdl(qk_norm_rope_kernel<kRpHalf>, grid, block, 0, st, p);
+  else e = launch_pdl(qk_norm_rope_kernel<kRpHalfOdd>, grid, block, 0, st, p);
   return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
