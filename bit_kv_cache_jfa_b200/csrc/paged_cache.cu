@@ -47,6 +47,17 @@ __device__ __forceinline__ GroupParams group_params(float mn, float mx, uint16_t
   return g;
 }
 
+// The rows of sequence `row` among the new ones: the first and how many.  A
+// range longer than its sequence is padded in front.
+__device__ __forceinline__ void new_rows(const PagedAppendParams& p, int row, int len, int& a, int& n) {
+  a = p.cu ? p.cu[row] : row * p.n_each;
+  n = p.cu ? p.cu[row + 1] - a : p.n_each;
+  if (n > len) {
+    a += n - len;
+    n = len;
+  }
+}
+
 // A CTA per (unit, KV head); a unit is one page of a row to be packed.  The
 // first unit of a row that gets tokens (there is one even when no page is
 // complete) also rewrites the row's tail, after it has read what it packs of
@@ -73,25 +84,24 @@ __global__ void __launch_bounds__(kPcThreads) paged_append_kernel(const __grid_c
   pdl_launch_dependents();
   int units = 0;
   if (tid < p.c.batch) {
-    const int a = p.cu ? p.cu[tid] : tid * p.n_each;
-    const int n_new = p.cu ? p.cu[tid + 1] - a : p.n_each;
-    const int n1 = p.c.seq_lens[tid];
-    if (n_new != 0 && (p.cu || n1 != 0)) {  // an empty sequence of a uniform append is idle
-      const int len = checked_len(n1, p.c.max_pages, p.flag);
-      if (a < 0 || n_new < 0 || a > p.n_total - n_new || n_new > len) {
-        set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
-      } else {
-        units = max(1, (split_point(len) - split_point(len - n_new)) / kKG);
-      }
+    const int len = checked_len(p.c.seq_lens[tid], p.c.max_pages, p.flag);
+    const int c0 = p.cu ? p.cu[tid] : 0, c1 = p.cu ? p.cu[tid + 1] : 0;
+    if (c0 < 0 || c1 < c0 || c1 > p.n_total) {
+      set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
+    } else {
+      int a, n_new;
+      new_rows(p, tid, len, a, n_new);
+      if (n_new > 0) units = max(1, (split_point(len) - split_point(len - n_new)) / kKG);
     }
   }
   batch_prefix(units, pre, wsum);
   const int x = blockIdx.x;
   if (x >= pre[kMaxBatch]) return;
   const int row = batch_find(pre, x), j = x - pre[row];
-  const int a = p.cu ? p.cu[row] : row * p.n_each;
-  const int n_new = p.cu ? p.cu[row + 1] - a : p.n_each;
-  const int n1 = p.c.seq_lens[row], n0 = n1 - n_new;
+  const int n1 = p.c.seq_lens[row];
+  int a, n_new;
+  new_rows(p, row, n1, a, n_new);
+  const int n0 = n1 - n_new;
   const int nq0 = split_point(n0), nq1 = split_point(n1);
   const size_t seg = (size_t)row * p.c.num_kv_heads + h;
   uint8_t* tail[2] = {reinterpret_cast<uint8_t*>(p.c.tail_k) + seg * kPgTailBytes,

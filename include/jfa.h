@@ -596,8 +596,9 @@ int jfa_paged_workspace_bytes(const jfa_paged* cache, size_t* bytes);
 /* Append rows.  Row range [cu[b], cu[b + 1]) of k_new / v_new (bf16
  * [n_total][H_kv][128], channels contiguous, strides in elements, multiples
  * of 8) holds sequence b's newest tokens; cu null: n_total / batch rows each
- * (n_total a multiple of batch), sequences of length 0 left alone.  seq_lens
- * are the lengths WITH the new tokens.  Groups that are complete are
+ * (n_total a multiple of batch).  seq_lens are the lengths WITH the new
+ * tokens; of a range longer than its sequence the last seq_lens[b] rows count
+ * (a batch padded in front; none of an idle sequence).  Groups that are complete are
  * quantized (jfa_pack_kv's rule) into the table's pages, the rest becomes the
  * tail.  cu: int32 [batch + 1], device.  One launch.  Stream-ordered. */
 int jfa_paged_append(const jfa_paged* cache, const uint16_t* k_new, int64_t k_tok, int64_t k_head,

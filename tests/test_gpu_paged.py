@@ -235,6 +235,23 @@ def test_uniform_append_leaves_idle_rows():
     assert torch.equal(cache.tail_k[1], before)
 
 
+@pytest.mark.parametrize("ranges", [False, True])
+def test_append_padded_in_front(ranges):
+    """Rows of one length for every sequence, the shorter ones padded in front."""
+    lens, wide, hkv = [130, 1, 0, 64, 200], 200, 2
+    table = jfa.PageTable(5, 12, 5)
+    cache = jfa.PagedKVCache(table, 2, hkv)
+    ws = jfa.PagedWorkspace(cache)
+    k, v = make_rows(5 * wide, hkv, 14)
+    rows = [(k[wide * (b + 1) - n:wide * (b + 1)], v[wide * (b + 1) - n:wide * (b + 1)]) for b, n in enumerate(lens)]
+    table.grow(lens)
+    cu = torch.arange(6, dtype=torch.int32, device="cuda") * wide if ranges else None
+    jfa.paged_append(cache, k.cuda(), v.cuda(), ws, cu)
+    torch.cuda.synchronize()
+    assert ws.error_flag(cache) == 0
+    check_cache(table, cache, rows)
+
+
 def test_append_ties_and_constant_groups():
     """Rows whose quotients lie on borders between codes, constant groups
     (scale 0), the type's smallest steps."""
