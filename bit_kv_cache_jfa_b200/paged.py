@@ -15,36 +15,49 @@ when no stream is given, and on the device that holds the cache.
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
 import heapq
 import math
+
+import torch
 
 from . import _lib
 from ._lib import JFA_ERR_INVALID_ARG, JfaError, Paged, Rope, check
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _torch():
-    import torch
-    return torch
+_BF16 = torch.bfloat16
+_SCALE = 1.0 / math.sqrt(_lib.HEAD_DIM)
 
 
 def _refuse(where: str, why: str):
     raise JfaError(JFA_ERR_INVALID_ARG, f"{where}: {why}")
 
 
-def _on(dev, stream):
-    """(guard that makes dev current, stream handle) of a call."""
-    cuda = _torch().cuda
-    guard = _NO_GUARD if cuda.current_device() == dev.index else cuda.device(dev)
+def _handle(dev, stream):
+    """Handle of a call's stream: the given one, else torch's current one on dev."""
     if stream is None:
-        stream = cuda.current_stream(dev)
-    return guard, stream if isinstance(stream, int) else stream.cuda_stream
+        return _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _run(where, dev, stream, *args):
+    """Call the library's ``where`` on dev and ``stream``.  These calls take
+    microseconds on the device: what the host adds is kept small (one look at
+    the current device and stream, no context manager when dev is current)."""
+    fn, st = getattr(_lib.load(), where), _handle(dev, stream)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status:
+        check(status, where)
+
+
+# The handle of a device's current stream without a Stream object (2 us) around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _int32(x, n, dev, where, name):
-    torch = _torch()
     if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous() or x.device != dev:
         _refuse(where, f"{name} must be {n} contiguous int32 on {dev}")
     return x.data_ptr()
@@ -52,19 +65,29 @@ def _int32(x, n, dev, where, name):
 
 def _rows(x, heads, dev, where, name):
     """Address and strides of bf16 rows [T][heads][128]."""
-    torch = _torch()
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != _lib.HEAD_DIM \
-            or x.device != dev or (x.stride(2) != 1 and x.numel()):
+    shape, strides = x.shape, x.stride()
+    if x.dtype != _BF16 or len(shape) != 3 or shape[1] != heads or shape[2] != 128 or x.device != dev \
+            or (strides[2] != 1 and x.numel()):
         _refuse(where, f"{name} must be bf16 [tokens, {heads}, {_lib.HEAD_DIM}] on {dev}, channels contiguous")
-    return x.data_ptr(), x.stride(0), x.stride(1)
+    return x.data_ptr(), strides[0], strides[1]
+
+
+def _given(x, shape, dev, where, name):
+    if x.shape != shape or x.dtype != _BF16 or x.device != dev or not x.is_contiguous():
+        _refuse(where, f"{name} must be contiguous bf16 {list(shape)} on {dev}")
 
 
 def _device(device):
-    torch = _torch()
     dev = torch.device(device)
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     return dev
+
+
+def _weight(w, dev, where, name):
+    if w.dtype != _BF16 or w.shape != (_lib.HEAD_DIM,) or w.device != dev or not w.is_contiguous():
+        _refuse(where, f"{name} must be bf16 [{_lib.HEAD_DIM}] on {dev}")
+    return w.data_ptr()
 
 
 class RotaryPlan:
@@ -127,9 +150,9 @@ class RotaryPlan:
         if not math.isfinite(self.amplitude):
             _refuse(where, "amplitude must be finite")
         turns = [round(x / (2 * math.pi) * 2.0**64) % 2**64 for x in f]   # in 2^-64 turns
-        torch = _torch()
         self.freq = torch.tensor([t - 2**64 if t >= 2**63 else t for t in turns], dtype=torch.int64,
                                  device=_device(device))
+        self.freq_ptr = self.freq.data_ptr()
 
 
 def qk_norm_rope(q, k, positions, plan: RotaryPlan, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -141,36 +164,34 @@ def qk_norm_rope(q, k, positions, plan: RotaryPlan, q_weight=None, k_weight=None
     are multiples of 8, channels contiguous); positions int32 or int64 [T];
     weights bf16 [128].  Returns (q, k) bf16, contiguous unless given; q_out=q
     and k_out=k work in place."""
-    torch = _torch()
     where = "qk_norm_rope"
     dev = plan.freq.device
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or qs[0] != ks[0]:
         _refuse(where, "q and k must be [tokens, heads, 128] of the same tokens")
-    t, h, hkv = q.shape[0], q.shape[1], k.shape[1]
-    qa, ka = _rows(q, h, dev, where, "q"), _rows(k, hkv, dev, where, "k")
+    t, h, hkv = qs[0], qs[1], ks[1]
+    qp, q_tok, q_head = _rows(q, h, dev, where, "q")
+    kp, k_tok, k_head = _rows(k, hkv, dev, where, "k")
     wide = positions.dtype == torch.int64
     if not (wide or positions.dtype == torch.int32) or positions.shape != (t,) or positions.device != dev \
             or not positions.is_contiguous():
         _refuse(where, f"positions must be {t} contiguous int32 or int64 on {dev}")
-    w = []
-    for x, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if x is not None and (x.dtype != torch.bfloat16 or x.shape != (_lib.HEAD_DIM,) or x.device != dev
-                              or not x.is_contiguous()):
-            _refuse(where, f"{name} must be bf16 [{_lib.HEAD_DIM}] on {dev}")
-        w.append(None if x is None else x.data_ptr())
+    qw = None if q_weight is None else _weight(q_weight, dev, where, "q_weight")
+    kw = None if k_weight is None else _weight(k_weight, dev, where, "k_weight")
     if q_out is None:
-        q_out = torch.empty((t, h, _lib.HEAD_DIM), dtype=torch.bfloat16, device=dev)
-    if k_out is None:
-        k_out = torch.empty((t, hkv, _lib.HEAD_DIM), dtype=torch.bfloat16, device=dev)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif q_out.shape != qs:
         _refuse(where, "outputs must have their inputs' shapes")
-    qo, ko = _rows(q_out, h, dev, where, "q_out"), _rows(k_out, hkv, dev, where, "k_out")
-    r = Rope(t, h, hkv, plan.rotary_dim, plan.interleaved, wide, eps, plan.amplitude, qa[0], ka[0], qo[0],
-             ko[0], qa[1], qa[2], ka[1], ka[2], qo[1], qo[2], ko[1], ko[2], w[0], w[1],
-             positions.data_ptr(), plan.freq.data_ptr())
-    guard, st = _on(dev, stream)
-    with guard:
-        check(_lib.jfa_qk_norm_rope(r, st), "jfa_qk_norm_rope")
+    if k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    elif k_out.shape != ks:
+        _refuse(where, "outputs must have their inputs' shapes")
+    qop, qo_tok, qo_head = _rows(q_out, h, dev, where, "q_out")
+    kop, ko_tok, ko_head = _rows(k_out, hkv, dev, where, "k_out")
+    r = Rope(t, h, hkv, plan.rotary_dim, plan.interleaved, wide, eps, plan.amplitude, qp, kp, qop, kop, q_tok,
+             q_head, k_tok, k_head, qo_tok, qo_head, ko_tok, ko_head, qw, kw, positions.data_ptr(),
+             plan.freq_ptr)
+    _run("jfa_qk_norm_rope", dev, stream, ctypes.byref(r))
     return q_out, k_out
 
 
@@ -184,7 +205,6 @@ class PageTable:
     Updates are enqueued on torch's current stream."""
 
     def __init__(self, batch: int, n_pages: int, max_pages: int, device="cuda"):
-        torch = _torch()
         if not 1 <= batch <= _lib.MAX_BATCH or n_pages < 1 or max_pages < 1:
             _refuse("PageTable", f"batch must be 1..{_lib.MAX_BATCH}, n_pages and max_pages at least 1")
         self.batch, self.n_pages, self.max_pages = batch, n_pages, max_pages
@@ -210,7 +230,6 @@ class PageTable:
 
     def _up(self, values):
         """Host ints to the device, ordered on the current stream."""
-        torch = _torch()
         return torch.tensor(values, dtype=torch.int32).to(self.device, non_blocking=True)
 
     def _store(self, cells=(), pages=()):
@@ -227,7 +246,6 @@ class PageTable:
         complete get pages; paged_append then brings the rows.  Returns the
         rows' ranges (int32 [batch + 1] on the device) for the second form.
         Without enough free pages or room in a row nothing changes."""
-        torch = _torch()
         uniform = isinstance(n_new, int)
         counts = [n_new if n else 0 for n in self.lens] if uniform else [int(n) for n in n_new]
         if len(counts) != self.batch or min(counts) < 0:
@@ -314,7 +332,6 @@ class PagedKVCache:
     its life): the pool of pages and the exact tail of each sequence."""
 
     def __init__(self, table: PageTable, num_heads: int, num_kv_heads: int):
-        torch = _torch()
         self.table, self.device = table, table.device
         self.num_heads, self.num_kv_heads = num_heads, num_kv_heads
         # sizes first: a bad geometry is refused before anything is allocated
@@ -329,6 +346,8 @@ class PagedKVCache:
         s.pages, s.tail_k, s.tail_v = (x.data_ptr() for x in (self.pages, self.tail_k, self.tail_v))
         s.table, s.seq_lens = table.table.data_ptr(), table.seq_lens.data_ptr()
 
+        self._ref = ctypes.byref(s)
+
     def struct(self) -> Paged:
         return self._struct
 
@@ -342,27 +361,24 @@ class PagedWorkspace:
     Calls that may run at the same time need one each."""
 
     def __init__(self, cache: PagedKVCache):
-        torch = _torch()
         self.buf = torch.zeros(cache.workspace_bytes, dtype=torch.uint8, device=cache.device)
+        self.ptr, self.nbytes, self.device = self.buf.data_ptr(), cache.workspace_bytes, self.buf.device
 
     def error_flag(self, cache: PagedKVCache, stream=None) -> int:
-        guard, st = _on(cache.device, stream)
-        with guard:
-            status, flag = _lib.jfa_paged_check_error(cache.struct(), self.buf, st)
-        if status not in (_lib.JFA_OK, _lib.JFA_ERR_DEVICE):
+        with torch.cuda.device(cache.device):
+            status, flag = _lib.jfa_paged_check_error(cache.struct(), self.buf, _handle(cache.device, stream))
+        if status != _lib.JFA_ERR_DEVICE:
             check(status, "jfa_paged_check_error")
         return flag
 
     def clear_error(self, cache: PagedKVCache, stream=None) -> None:
-        guard, st = _on(cache.device, stream)
-        with guard:
-            check(_lib.jfa_paged_clear_error(cache.struct(), self.buf, st), "jfa_paged_clear_error")
+        _run("jfa_paged_clear_error", cache.device, stream, cache._ref, self.ptr)
 
 
 def _ws(cache, ws, where):
-    if ws.buf.numel() < cache.workspace_bytes or ws.buf.device != cache.device:
+    if ws.nbytes < cache.workspace_bytes or ws.device != cache.device:
         _refuse(where, f"workspace must hold {cache.workspace_bytes} bytes on {cache.device}")
-    return ws.buf
+    return ws.ptr
 
 
 def paged_append(cache: PagedKVCache, k, v, ws: PagedWorkspace, cu=None, stream=None) -> None:
@@ -377,10 +393,7 @@ def paged_append(cache: PagedKVCache, k, v, ws: PagedWorkspace, cu=None, stream=
     if k.shape[0] != v.shape[0]:
         _refuse(where, "k and v must hold the same tokens")
     cup = None if cu is None else _int32(cu, batch + 1, dev, where, "cu")
-    guard, st = _on(dev, stream)
-    with guard:
-        check(_lib.jfa_paged_append(cache.struct(), *ka, *va, cup, k.shape[0], _ws(cache, ws, where), st),
-              "jfa_paged_append")
+    _run("jfa_paged_append", dev, stream, cache._ref, *ka, *va, cup, k.shape[0], _ws(cache, ws, where))
 
 
 def paged_gather(cache: PagedKVCache, cu, total: int, ws: PagedWorkspace, start=None, k_out=None, v_out=None,
@@ -388,25 +401,23 @@ def paged_gather(cache: PagedKVCache, cu, total: int, ws: PagedWorkspace, start=
     """Read rows back: tokens start[b] (from 0 on without start) and following
     of sequence b into rows cu[b] .. cu[b + 1] - 1 of bf16 [total, H_kv, 128];
     rows in no range are left as they are (unset in a new output).  Returns (k, v)."""
-    torch = _torch()
     where = "paged_gather"
     dev, batch = cache.device, cache.table.batch
     shape = (total, cache.num_kv_heads, _lib.HEAD_DIM)
     if total < 0:
         _refuse(where, "total must not be negative")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = torch.empty(shape, dtype=_BF16, device=dev)
+    else:
+        _given(k_out, shape, dev, where, "k_out")
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if x.shape != shape or x.dtype != torch.bfloat16 or x.device != dev or not x.is_contiguous():
-            _refuse(where, f"{name} must be contiguous bf16 {list(shape)} on {dev}")
+        v_out = torch.empty_like(k_out)
+    else:
+        _given(v_out, shape, dev, where, "v_out")
     cup = _int32(cu, batch + 1, dev, where, "cu")
     stp = None if start is None else _int32(start, batch, dev, where, "start")
-    guard, st = _on(dev, stream)
-    with guard:
-        check(_lib.jfa_paged_gather(cache.struct(), cup, stp, total, k_out, v_out, _ws(cache, ws, where), st),
-              "jfa_paged_gather")
+    _run("jfa_paged_gather", dev, stream, cache._ref, cup, stp, total, k_out.data_ptr(), v_out.data_ptr(),
+         _ws(cache, ws, where))
     return k_out, v_out
 
 
@@ -418,26 +429,24 @@ def paged_attend(cache: PagedKVCache, q, ws: PagedWorkspace, scale=None, window:
     q: bf16 [B, H, 128] (heads contiguous, any row stride that is a multiple
     of 8).  Returns out bf16 [B, H, 128], zeros for an idle sequence; lse (fp32
     [B, H], if given) gets the natural logarithm of the softmax's sum."""
-    torch = _torch()
     where = "paged_attend"
     dev, batch, heads = cache.device, cache.table.batch, cache.num_heads
     qp, q_row, q_head = _rows(q, heads, dev, where, "q")
     if q.shape[0] != batch or (q_head != _lib.HEAD_DIM and heads > 1):
         _refuse(where, f"q must hold {batch} tokens, its heads contiguous")
     if out is None:
-        out = torch.empty((batch, heads, _lib.HEAD_DIM), dtype=torch.bfloat16, device=dev)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous():
-        _refuse(where, f"out must be contiguous bf16 {list(q.shape)} on {dev}")
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _given(out, q.shape, dev, where, "out")
     if lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != dev
                             or not lse.is_contiguous()):
         _refuse(where, f"lse must be contiguous fp32 [{batch}, {heads}] on {dev}")
-    scale = 1.0 / math.sqrt(_lib.HEAD_DIM) if scale is None else float(scale)
-    if not (scale > 0 and math.isfinite(scale)):
+    if scale is None:
+        scale = _SCALE
+    elif not (scale > 0 and math.isfinite(scale)):
         _refuse(where, "scale must be positive and finite")
-    guard, st = _on(dev, stream)
-    with guard:
-        check(_lib.jfa_paged_attend(cache.struct(), qp, q_row, scale, window, sinks, _ws(cache, ws, where),
-                                    out, lse, st), "jfa_paged_attend")
+    _run("jfa_paged_attend", dev, stream, cache._ref, qp, q_row, scale, window, sinks, _ws(cache, ws, where),
+         out.data_ptr(), None if lse is None else lse.data_ptr())
     return out
 
 
@@ -450,9 +459,7 @@ def paged_fork(cache: PagedKVCache, pairs, ws: PagedWorkspace, stream=None) -> N
     if n > cache.table.batch:
         _refuse(where, f"{n} pairs for {cache.table.batch} sequences")
     p = _int32(pairs, 2 * n, cache.device, where, "pairs")
-    guard, st = _on(cache.device, stream)
-    with guard:
-        check(_lib.jfa_paged_fork(cache.struct(), p, n, _ws(cache, ws, where), st), "jfa_paged_fork")
+    _run("jfa_paged_fork", cache.device, stream, cache._ref, p, n, _ws(cache, ws, where))
 
 
 def paged_move(cache: PagedKVCache, moves, ws: PagedWorkspace, remap=None, stream=None) -> None:
@@ -466,10 +473,7 @@ def paged_move(cache: PagedKVCache, moves, ws: PagedWorkspace, remap=None, strea
         _refuse(where, f"{n} moves for {cache.table.n_pages} pages")
     m = _int32(moves, 2 * n, cache.device, where, "moves")
     r = None if remap is None else _int32(remap, cache.table.n_pages, cache.device, where, "remap")
-    guard, st = _on(cache.device, stream)
-    with guard:
-        check(_lib.jfa_paged_move(cache.struct(), m if n else None, n, r, _ws(cache, ws, where), st),
-              "jfa_paged_move")
+    _run("jfa_paged_move", cache.device, stream, cache._ref, m if n else None, n, r, _ws(cache, ws, where))
 
 
 def paged_decode_step(cache: PagedKVCache, q, k, v, positions, plan: RotaryPlan, ws: PagedWorkspace,
