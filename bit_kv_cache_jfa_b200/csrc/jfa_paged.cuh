@@ -28,7 +28,7 @@ JFA_HD int tail_chunk(int t, int c) { return t * kPgRow + ((c ^ (t & 7)) << 4); 
 // Workspace: the error flag, a ticket per (sequence, KV head) (zero between
 // calls) and the attention's partials: two per CTA, and one per warp.
 constexpr int kPgMaxCtas = 192;
-constexpr int kPgWarps = 16;
+constexpr int kPgWarps = 12;
 constexpr int kPgPart = kMaxG * kPartStride;  // floats of one partial: per head m, l, pad2, acc[128]
 struct PagedWs {
   size_t off_flag, off_ticket, off_cta, off_warp, total;

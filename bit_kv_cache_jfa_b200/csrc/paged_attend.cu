@@ -27,10 +27,12 @@
 // The query is scaled by a power of two to [1/8, 1/4) first, so that q s,
 // times the 16 of the codes' position, stays in fp16's range at every scale a
 // record can hold (131008 / 15).  The weights are taken against a reference
-// 2^e under the running maximum, p_t = 2^(u - max + e): e is 15 where the
-// value scales are below 2 and falls (for the rest of the segment) where a
-// larger one would take p_t s_tj past fp16, so that weights down to 2^-29 of
-// the largest keep their 11 bits, however many tokens share the mass.
+// r, p_t = 2^(u - r), set so that the largest is at most 2^e: e is 15 where
+// the value scales are below 2 and falls (for the rest of the segment) where a
+// larger one would take p_t s_tj past fp16.  r rises only when a weight would
+// pass 2^e, and then to leave it at 2^(e - 5): sums are rarely scaled again,
+// and weights down to 2^-24 of the largest keep their 11 bits, however many
+// tokens share the mass.
 #include "jfa_approx.cuh"
 #include "jfa_paged.cuh"
 
@@ -42,7 +44,8 @@ constexpr int kPaV = 1024 + 4096;  // the same of the values
 // Per warp two key buffers and one value buffer: while the values of a group
 // are used the next keys have arrived, and while keys are used the values
 // arrive.  16 warps hold about 150 KB in flight per SM.
-constexpr int kPaWarpBytes = 2 * kPaK + kPaV;
+constexpr int kPaKBuf = 2;
+constexpr int kPaWarpBytes = kPaKBuf * kPaK + kPaV;
 constexpr int kPaSmem = kPgWarps * kPaWarpBytes;
 constexpr int kPaTailTok = 16;                      // tokens of a tail item
 constexpr int kPaTailBytes = kPaTailTok * kPgRow;   // of K or V
@@ -50,6 +53,10 @@ constexpr int kPaMinItems = 8;                      // items per CTA, at least
 static_assert(kPaTailBytes <= kPaK && kPaTailBytes <= kPaV, "a tail item fits the buffers");
 static_assert(kPgPart * 4 <= kPaWarpBytes, "a warp's partial fits its buffers");
 static_assert(kPaSmem + 3072 <= 227 * 1024, "shared memory");
+// Room that a raised reference leaves under the largest weight that fits: a
+// maximum that grows by less than 2^5 raises nothing, so that after a warp's
+// first group the sums are rarely scaled again.
+constexpr float kPaRoom = 5.f;
 constexpr float kPaLn2 = 0.6931471805599453f;
 // Where a running maximum starts: finite, so that a masked logit (-inf) minus
 // it is -inf and its weight 0.
@@ -90,6 +97,32 @@ __device__ __forceinline__ RowView row_view(int n, int window, int sinks) {
   return v;
 }
 
+// x / d and x % d for a quotient below 2^20 (here: KV heads), from an fp32
+// quotient that is off by one at most.
+__device__ __forceinline__ int div_small(int x, int d, int& rem) {
+  int q = (int)__fdividef((float)x, (float)d);
+  rem = x - q * d;
+  if (rem < 0) {
+    --q;
+    rem += d;
+  } else if (rem >= d) {
+    ++q;
+    rem -= d;
+  }
+  return q;
+}
+
+// A range of n cut into parts whose sizes differ by one at most, the longer first.
+struct Cut {
+  int q, r;
+  __device__ __forceinline__ Cut(int n, int parts) : q(n / parts), r(n % parts) {}
+  __device__ __forceinline__ int begin(int i) const { return i * q + min(i, r); }
+  __device__ __forceinline__ int part_of(int x) const {
+    const int longer = r * (q + 1);
+    return x < longer ? x / (q + 1) : r + (x - longer) / q;
+  }
+};
+
 enum : int { kItTail = 1, kItMask = 2, kItSkip = 4, kItFirst = 8, kItLast = 16 };
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -117,6 +150,12 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// a b - c
+__device__ __forceinline__ uint32_t h2_rest(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
+                            __hneg2(*reinterpret_cast<__half2*>(&c)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -130,7 +169,7 @@ __device__ __forceinline__ uint32_t half_mask(bool lo, bool hi) {
 
 // Persistent: the items of all (sequence, KV head) segments, in a row, are cut
 // into equal ranges, one per CTA and in it one per warp.  A warp carries the
-// running maximum, mass and weighted values of its current segment; what it
+// reference, mass and weighted values of its current segment; what it
 // finishes alone it writes out, the rest is merged in fixed order (so results
 // do not depend on timing): over the CTA's warps in shared memory, over CTAs
 // by the last one to add its items to the segment's ticket.
@@ -138,17 +177,18 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   extern __shared__ __align__(128) uint8_t pa_smem[];
   __shared__ int pre[kMaxBatch + 1];
   __shared__ int wsum[kMaxBatch / 32];
-  __shared__ uint64_t bars[kPgWarps][3];
+  __shared__ int lens[kMaxBatch];
+  __shared__ uint64_t bars[kPgWarps][kPaKBuf + 1];
   __shared__ int tail_seg[kPgWarps + 1], head_seg[kPgWarps + 1];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int hkv = p.c.num_kv_heads, G = p.G, H = p.c.num_heads;
   uint8_t* ring = pa_smem + warp * kPaWarpBytes;
   uint64_t* bar_k = bars[warp];
-  uint64_t* bar_v = &bars[warp][2];
+  uint64_t* bar_v = &bars[warp][kPaKBuf];
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) mbar_init(&bars[warp][i], 1);
+    for (int i = 0; i <= kPaKBuf; ++i) mbar_init(&bars[warp][i], 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -157,12 +197,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     if (tid < p.c.batch) {
       const int n = checked_len(p.c.seq_lens[tid], p.c.max_pages, p.flag);
       items = row_view(n, p.window, p.sinks).items * hkv;
+      lens[tid] = n;
     }
     batch_prefix(items, pre, wsum);
   }
-  auto row_of = [&](int row) {
-    return row_view(checked_len(p.c.seq_lens[row], p.c.max_pages, nullptr), p.window, p.sinks);
-  };
+  auto row_of = [&](int row) { return row_view(lens[row], p.window, p.sinks); };
   const int T = pre[kMaxBatch];
   // sequences that show nothing: zeros, spread over the CTAs
   for (int row = blockIdx.x; row < p.c.batch; row += gridDim.x) {
@@ -174,10 +213,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   }
   const int C = min((int)gridDim.x, (T + kPaMinItems - 1) / kPaMinItems);
   if ((int)blockIdx.x >= C) return;
-  const int r0 = (int)((long long)blockIdx.x * T / C), r1 = (int)((long long)(blockIdx.x + 1) * T / C);
+  const Cut ctas(T, C);
+  const int r0 = ctas.begin(blockIdx.x), r1 = ctas.begin(blockIdx.x + 1);
   const int nw = min(kPgWarps, r1 - r0);  // the first nw warps have items
-  const int i0 = warp < nw ? r0 + (int)((long long)(r1 - r0) * warp / nw) : r1;
-  const int i1 = warp < nw ? r0 + (int)((long long)(r1 - r0) * (warp + 1) / nw) : r1;
+  const Cut warps(r1 - r0, nw);
+  const int i0 = warp < nw ? r0 + warps.begin(warp) : r1, i1 = warp < nw ? r0 + warps.begin(warp + 1) : r1;
 
   // ---- item descriptors: lane l holds those of item base + l
   int base = i0;
@@ -188,7 +228,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     if (x < i1) {
       const int row = batch_find(pre, x);
       const RowView v = row_of(row);
-      const int rel = x - pre[row], head = rel / v.items, j = rel % v.items;
+      int j;
+      const int head = div_small(x - pre[row], v.items, j);
       d_seg = row * hkv + head;
       d_kind = (j == 0 ? kItFirst : 0) | (j == v.items - 1 ? kItLast : 0);
       const int npk = v.gs + v.ng - v.gw;
@@ -230,7 +271,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
                                : static_cast<const uint8_t*>(p.c.pages) + kPaK) + d_off;
       const uint32_t bytes = tl ? kPaTailBytes : kPaV;
       mbar_expect_tx(bar_v, bytes);
-      bulk_g2s(ring + 2 * kPaK, src, bytes, bar_v, pol);
+      bulk_g2s(ring + kPaKBuf * kPaK, src, bytes, bar_v, pol);
     }
   };
 
@@ -239,21 +280,26 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   float dz[4];       // rows 0-3: zero-point sums per channel group, row 4: mass
   float m_run[2], kap[2];  // reference (running maximum - sh), kappa * 2^x of the query's scaling
   int sh = 15;             // e of the weights' reference
-  uint32_t q2[16];   // B fragment of the scaled query, head gid
+  uint32_t qf[16] = {};  // B fragment of the scaled query, head gid, times the codes' position factor
   int seg = 0;
   bool own_start = false;  // the segment's first item was this warp's
-  RowView rv;
+  RowView rv = {};
   int my_head_seg = -1, my_tail_seg = -1;
 
-  auto reset = [&](int s) {
-    seg = s;
-    const int row = s / hkv, head = s % hkv;
-    rv = row_of(row);
+  auto reset_sums = [&]() {
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     dz[0] = dz[1] = dz[2] = dz[3] = 0.f;
     m_run[0] = m_run[1] = kPaMin;
+    kap[0] = kap[1] = 0.f;
     sh = 15;
+  };
+  auto reset = [&](int s) {
+    seg = s;
+    int head;
+    const int row = div_small(s, hkv, head);
+    rv = row_of(row);
+    reset_sums();
     const bool ok = gid < G;
     const uint16_t* qr = p.q + (int64_t)row * p.q_row + (size_t)(head * G + (ok ? gid : 0)) * kD;
     uint32_t w[16];
@@ -271,7 +317,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     const int x = ex == 0 || ex >= 250 ? 0 : ex - 127 + 3;
     const float down = __uint_as_float((uint32_t)(127 - x) << 23), up = __uint_as_float((uint32_t)(127 + x) << 23);
 #pragma unroll
-    for (int pp = 0; pp < 16; ++pp) q2[pp] = pack_h2(bf_lo(w[pp]) * down, bf_hi(w[pp]) * down);
+    for (int pp = 0; pp < 16; ++pp) {
+      const float f = pp < 8 ? 16.f * down : down;  // KeyPos<4>::factor
+      qf[pp] = pack_h2(bf_lo(w[pp]) * f, bf_hi(w[pp]) * f);
+    }
     kap[0] = p.kappa * __shfl_sync(0xFFFFFFFFu, up, 8 * tig);
     kap[1] = p.kappa * __shfl_sync(0xFFFFFFFFu, up, 8 * tig + 4);
   };
@@ -301,7 +350,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     }
   };
   auto store_out = [&]() {
-    const int row = seg / hkv, head = seg % hkv;
+    int head;
+    const int row = div_small(seg, hkv, head);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float l = __shfl_sync(0xFFFFFFFFu, dz[e], 16 + tig);
@@ -339,31 +389,43 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     dz[2] *= a0;
     dz[3] *= a1;
   };
-  // the lane's largest logits of heads 2 tig + e: raises the references
+  // the lane's largest logits of heads 2 tig + e: where one is more than 2^sh
+  // over its reference, the references go to kPaRoom below 2^sh over the largest
   auto raise_max = [&](float mx0, float mx1) {
+    const float top = (float)sh;
+    if (__any_sync(0xFFFFFFFFu, mx0 > m_run[0] + top || mx1 > m_run[1] + top)) {
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, o));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, o));
+      for (int o = 4; o < 32; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, o));
+      }
+      rescale(mx0 > m_run[0] + top ? mx0 - (top - kPaRoom) : m_run[0],
+              mx1 > m_run[1] + top ? mx1 - (top - kPaRoom) : m_run[1]);
     }
-    mx0 -= (float)sh;
-    mx1 -= (float)sh;
-    if (__any_sync(0xFFFFFFFFu, mx0 > m_run[0] || mx1 > m_run[1]))
-      rescale(fmaxf(m_run[0], mx0), fmaxf(m_run[1], mx1));
   };
 
+  // Every warp's first keys are requested before any other copy, so that the
+  // first products start when a third of the buffers has been filled.  While
+  // they are on their way the loop's body runs once on nothing (a group with
+  // every token masked, whatever the buffers hold; reset() drops its sums):
+  // its instructions are fetched by then.
+  reset_sums();
   if (i0 < i1) {
     describe();
     __syncwarp();
     issue_k(i0, 0);
+  }
+  __syncthreads();
+  if (i0 < i1) {
     issue_v(i0);
-    if (i0 + 1 < i1) issue_k(i0 + 1, 1);
+    for (int x = 1; x < kPaKBuf; ++x)
+      if (i0 + x < i1) issue_k(i0 + x, x);
   }
   int st = 0;
   uint32_t par_k = 0u, par_v = 0u;  // bit s: parity of key buffer s
   bool failed = false;
   for (int i = i0; i < i1; ++i) {
-    if (i + 2 - base >= 32 && i + 2 < i1) {  // the next keys' descriptor is needed below
+    if (i + kPaKBuf - base >= 32 && i + kPaKBuf < i1) {  // the next keys' descriptor is needed below
       base = i;
       describe();
       __syncwarp();
@@ -383,51 +445,66 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     failed |= !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar_k[st], (par_k >> st) & 1u));
     par_k ^= 1u << st;
     const uint8_t* rk = ring + st * kPaK;
-    const uint8_t* rvb = ring + 2 * kPaK;
+    const uint8_t* rvb = ring + kPaKBuf * kPaK;
     if (!(kind & kItTail)) {
-      // ---- B operand fp16(q s F), the remainders' share and the bias
-      uint32_t qb[16];
-      float bk[2];
-      {
-        uint32_t sk[16], zk[16];
-        key_sz(rk, tig, sk, zk);
-        float bz[4] = {0.f, 0.f, 0.f, 0.f}, cr[4] = {0.f, 0.f, 0.f, 0.f};
+      // ---- logits (log2 units) u[mt][2 r + e]: token 16 mt + gid + 8 r, head
+      // 2 tig + e.  Half of the code words at a time (slots 4 h .. 4 h + 3 in
+      // their low, 8 more in their high nibbles): the B operand fp16(q s F) of
+      // these slots, the bias (the remainders' share and the zero points), and
+      // four chains of MMAs, one an m-tile.
+      float u[4][4] = {};
+      float bz[2][4] = {}, cr[4] = {};  // bz[0]: slots 0-7, with the factor 16
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma16816(bz, zk[2 * ks], zk[2 * ks], zk[2 * ks + 1], zk[2 * ks + 1], q2[2 * ks], q2[2 * ks + 1]);
-        uint32_t lo[16];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t qb[2][4];
 #pragma unroll
-        for (int pp = 0; pp < 16; ++pp) {
-          const uint32_t qf = h2_mul(q2[pp], KeyPos<4>::factor(pp));
-          qb[pp] = h2_mul(qf, sk[pp]);
-          lo[pp] = h2_fma(qf, sk[pp], qb[pp] ^ 0x80008000u);
+        for (int n = 0; n < 2; ++n) {  // slots 4 h + 8 n ..
+          const int i4 = h + 2 * n;
+          const uint4 sv = *reinterpret_cast<const uint4*>(rk + i4 * 64 + tig * 16);
+          const uint4 zv = *reinterpret_cast<const uint4*>(rk + (4 + i4) * 64 + tig * 16);
+          const uint32_t sk[4] = {sv.x, sv.y, sv.z, sv.w}, zk[4] = {zv.x, zv.y, zv.z, zv.w};
+          const uint32_t c15 = n == 0 ? 0x000F000Fu : 0x00F000F0u;  // twice 7.5, at the codes' bit position
+          uint32_t lo[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            qb[n][x] = h2_mul(qf[4 * i4 + x], sk[x]);
+            lo[x] = h2_rest(qf[4 * i4 + x], sk[x], qb[n][x]);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; x += 2) {
+            mma16816(bz[n], zk[x], zk[x], zk[x + 1], zk[x + 1], qf[4 * i4 + x], qf[4 * i4 + x + 1]);
+            mma16816(cr, c15, c15, c15, c15, lo[x], lo[x + 1]);
+          }
         }
-        // twice 7.5, at the codes' bit position: 0 for slots 0-7, 4 for 8-15
+        uint32_t w[4][4];
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t c15 = ks < 4 ? 0x000F000Fu : 0x00F000F0u;
-          mma16816(cr, c15, c15, c15, c15, lo[2 * ks], lo[2 * ks + 1]);
+        for (int mt = 0; mt < 4; ++mt) {
+          const uint4 c = *reinterpret_cast<const uint4*>(rk + 512 + mt * 1024 + lane * 32 + 16 * h);
+          w[mt][0] = c.x, w[mt][1] = c.y, w[mt][2] = c.z, w[mt][3] = c.w;
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) bk[e] = fmaf(cr[e], 0.5f * KeyPos<4>::unscale, bz[e]) * kap[e];
+        for (int x = 0; x < 4; x += 2)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t mask = 0x000F000Fu << (4 * n);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+              mma16816(u[mt], w[mt][x] & mask, (w[mt][x] >> 8) & mask, w[mt][x + 1] & mask,
+                       (w[mt][x + 1] >> 8) & mask, qb[n][x], qb[n][x + 1]);
+          }
       }
-      // ---- logits (log2 units) u[mt][2 r + e]: token 16 mt + gid + 8 r, head 2 tig + e
-      float u[4][4];
-      const float ku[2] = {kap[0] * KeyPos<4>::unscale, kap[1] * KeyPos<4>::unscale};
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        const uint8_t* kp = rk + 512 + mt * 1024 + lane * 32;
-        const uint4 c0 = *reinterpret_cast<const uint4*>(kp), c1 = *reinterpret_cast<const uint4*>(kp + 16);
-        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        uint32_t a[16][2];
-        key_afrag<4>(w, a);
-        float d[4];
-        qk_chain(a, qb, d);
+      for (int e = 0; e < 2; ++e) {
+        const float bk = (fmaf(cr[e], 0.5f * KeyPos<4>::unscale, bz[1][e]) + bz[0][e] * 0.0625f) * kap[e];
+        const float ku = kap[e] * KeyPos<4>::unscale;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) u[mt][x] = fmaf(d[x], ku[x & 1], bk[x & 1]);
+        for (int mt = 0; mt < 4; ++mt) {
+          u[mt][e] = fmaf(u[mt][e], ku, bk);
+          u[mt][2 + e] = fmaf(u[mt][2 + e], ku, bk);
+        }
       }
       __syncwarp();
-      if (i + 2 < i1) issue_k(i + 2, st);
+      if (i + kPaKBuf < i1) issue_k(i + kPaKBuf, st);
       if (kind & kItMask) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
@@ -516,7 +593,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       uint32_t qw[16];
       {
         const bool ok = gid < G;
-        const uint16_t* qr = p.q + (int64_t)(seg / hkv) * p.q_row + (size_t)((seg % hkv) * G + (ok ? gid : 0)) * kD;
+        int head;
+        const int row = div_small(seg, hkv, head);
+        const uint16_t* qr = p.q + (int64_t)row * p.q_row + (size_t)(head * G + (ok ? gid : 0)) * kD;
 #pragma unroll
         for (int pp = 0; pp < 16; ++pp)
           qw[pp] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * (pp >> 1) + 2 * tig + 8 * (pp & 1)) : 0u;
@@ -530,7 +609,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         mma_bf16(d, a[0], a[1], a[2], a[3], qw[2 * ks], qw[2 * ks + 1]);
       }
       __syncwarp();
-      if (i + 2 < i1) issue_k(i + 2, st);
+      if (i + kPaKBuf < i1) issue_k(i + kPaKBuf, st);
       float u[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) u[x] = visible(t0 + gid + 8 * (x >> 1)) ? d[x] * p.kappa : -INFINITY;
@@ -564,8 +643,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       }
     }
     __syncwarp();
+    st = st + 1 == kPaKBuf ? 0 : st + 1;
     if (i + 1 < i1) issue_v(i + 1);
-    st ^= 1;
     if (kind & kItLast) {
       if (own_start) {
         store_out();
@@ -592,112 +671,152 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   // ended a segment of the CTA before.  A warp takes a (run, head) at a time,
   // a lane 4 channels.
   auto seg_range = [&](int s, int& sa, int& sb) {
-    const int row = s / hkv, items = (pre[row + 1] - pre[row]) / hkv;
-    sa = pre[row] + (s % hkv) * items;
+    int head;
+    const int row = div_small(s, hkv, head), items = row_of(row).items;
+    sa = pre[row] + head * items;
     sb = sa + items;
   };
   auto smem_part = [&](int w) { return reinterpret_cast<const float*>(pa_smem + w * kPaWarpBytes); };
   auto gmem_part = [&](int w) { return p.part_warp + ((size_t)blockIdx.x * kPgWarps + w) * kPgPart; };
   auto finish = [&](int s, int h, float M, float L, float4 O) {
-    const int row = s / hkv, head = s % hkv;
+    int head;
+    const int row = div_small(s, hkv, head);
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const size_t at = (size_t)row * H + head * G + h;
     *reinterpret_cast<uint2*>(p.out + at * kD + 4 * lane) =
         make_uint2(pack_b2(O.x * inv, O.y * inv), pack_b2(O.z * inv, O.w * inv));
     if (lane == 0 && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPaLn2;
   };
-  for (int c = warp; c < (kPgWarps + 1) * G; c += kPgWarps) {
-    const int run = c / G, h = c % G;  // run 0: warp 0's ended segment; run w + 1 begins at warp w
-    int s, w0, w1, wh;                 // shared partials w0 .. w1 - 1 and, if wh >= 0, warp wh's in the workspace
-    if (run == 0) {
-      s = head_seg[0];
-      w0 = w1 = 0;
-      wh = 0;
-    } else {
-      w0 = run - 1;
-      s = tail_seg[w0];
-      if (w0 > 0 && tail_seg[w0 - 1] == s) s = -1;
-      w1 = w0 + 1;
-      while (w1 < kPgWarps && tail_seg[w1] == s) ++w1;
-      wh = head_seg[w1] == s ? w1 : -1;
-    }
-    if (s < 0) continue;
-    float M = kPaMin;
-    for (int w = w0; w < w1; ++w) M = fmaxf(M, smem_part(w)[h * kPartStride]);
-    if (wh >= 0) M = fmaxf(M, gmem_part(wh)[h * kPartStride]);
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float* src) {
-      const float f = exp2f(src[0] - M);
-      const float4 v = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
-      L = fmaf(src[1], f, L);
-      O.x = fmaf(v.x, f, O.x);
-      O.y = fmaf(v.y, f, O.y);
-      O.z = fmaf(v.z, f, O.z);
-      O.w = fmaf(v.w, f, O.w);
-    };
-    for (int w = w0; w < w1; ++w) add(smem_part(w) + h * kPartStride);
-    if (wh >= 0) add(gmem_part(wh) + h * kPartStride);
-    int sa, sb;
-    seg_range(s, sa, sb);
-    if (sa >= r0 && sb <= r1) {
-      finish(s, h, M, L, O);
-    } else {
-      float* dst = p.part_cta + ((size_t)blockIdx.x * 2 + (sa < r0 ? 0 : 1)) * kPgPart + h * kPartStride;
-      if (lane == 0) {
-        dst[0] = M;
-        dst[1] = L;
+  {
+    const int ts = lane < kPgWarps ? tail_seg[lane] : -1;
+    const int before = __shfl_up_sync(0xFFFFFFFFu, ts, 1);
+    const uint32_t starts = __ballot_sync(0xFFFFFFFFu, ts >= 0 && (lane == 0 || before != ts));
+    const int head0 = head_seg[0], nruns = __popc(starts) + (head0 >= 0);
+    for (int c = warp; c < nruns * G; c += kPgWarps) {
+      const int run = c / G, h = c % G;
+      // shared partials of the warps in mask and, if wh >= 0, warp wh's in the workspace
+      int sg, wh;
+      uint32_t mask = 0u;
+      if (run == __popc(starts)) {
+        sg = head0;
+        wh = 0;
+      } else {
+        const int w0 = __fns(starts, 0, run + 1);
+        sg = __shfl_sync(0xFFFFFFFFu, ts, w0);
+        mask = __ballot_sync(0xFFFFFFFFu, ts == sg);
+        const int w1 = w0 + __popc(mask);
+        wh = head_seg[w1] == sg ? w1 : -1;
       }
-      *reinterpret_cast<float4*>(dst + 4 + 4 * lane) = O;
-    }
-  }
-
-  // ---- the segments at the range's ends that other CTAs share
-  __threadfence();
-  __syncthreads();
-#pragma unroll 1
-  for (int end = 0; end < 2; ++end) {
-    const int x = end == 0 ? r0 : r1 - 1;
-    const int row = batch_find(pre, x), items = (pre[row + 1] - pre[row]) / hkv;
-    const int s = row * hkv + (x - pre[row]) / items;
-    int sa, sb;
-    seg_range(s, sa, sb);
-    if (sa >= r0 && sb <= r1) continue;      // finished here
-    if (end == 1 && sa <= r0) continue;      // one segment fills the range
-    if (tid == 0) {
-      const uint32_t mine = (uint32_t)(min(sb, r1) - max(sa, r0));
-      s_last = atomicAdd(&p.ticket[s], mine) + mine == (uint32_t)(sb - sa);
-    }
-    __syncthreads();
-    const bool last = s_last != 0;
-    __syncthreads();
-    if (!last) continue;
-    __threadfence();
-    const int ca = (int)(((long long)(sa + 1) * C - 1) / T), cb = (int)(((long long)sb * C - 1) / T);
-    // G heads, 16 / G warps each on every so-manieth CTA's partial
-    const int per = kPgWarps / G, h = warp % G, sub = warp / G;
-    auto part = [&](int c) {
-      const int rc = (int)((long long)c * T / C);
-      return p.part_cta + ((size_t)c * 2 + (sa < rc ? 0 : 1)) * kPgPart + h * kPartStride;
-    };
-    float* buf = reinterpret_cast<float*>(pa_smem) + warp * kPartStride;
-    if (sub < per) {
-      float M = kPaMin;
-      for (int c = ca + sub + per * lane; c <= cb; c += per * 32) M = fmaxf(M, __ldcg(part(c)));
+      // a lane takes one partial's maximum and mass, then every lane 4 channels
+      const bool mine = (mask >> lane) & 1u;
+      const float* pl = smem_part(min(lane, kPgWarps - 1)) + h * kPartStride;
+      const float* pg = gmem_part(wh < 0 ? 0 : wh) + h * kPartStride;
+      float4 og = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mg = kPaMin, lg = 0.f;
+      if (wh >= 0) {
+        mg = pg[0];
+        lg = pg[1];
+        og = *reinterpret_cast<const float4*>(pg + 4 + 4 * lane);
+      }
+      const float ml = mine ? pl[0] : kPaMin;
+      float M = ml;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-      float L = 0.f;
-      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+      M = fmaxf(__shfl_sync(0xFFFFFFFFu, M, 0), mg);
+      const float fl = mine ? exp2f(ml - M) : 0.f, fg = wh >= 0 ? exp2f(mg - M) : 0.f;
+      float L = mine ? fl * pl[1] : 0.f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+      L = fmaf(lg, fg, __shfl_sync(0xFFFFFFFFu, L, 0));
+      float4 O = make_float4(og.x * fg, og.y * fg, og.z * fg, og.w * fg);
 #pragma unroll 4
-      for (int c = ca + sub; c <= cb; c += per) {
-        const float* src = part(c);
-        const float f = exp2f(__ldcg(src) - M);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + 4 + 4 * lane));
-        L = fmaf(__ldcg(src + 1), f, L);
+      for (uint32_t m = mask; m;) {
+        const int w = __ffs(m) - 1;
+        m &= m - 1;
+        const float f = __shfl_sync(0xFFFFFFFFu, fl, w);
+        const float4 v = *reinterpret_cast<const float4*>(smem_part(w) + h * kPartStride + 4 + 4 * lane);
         O.x = fmaf(v.x, f, O.x);
         O.y = fmaf(v.y, f, O.y);
         O.z = fmaf(v.z, f, O.z);
         O.w = fmaf(v.w, f, O.w);
+      }
+      int sa, sb;
+      seg_range(sg, sa, sb);
+      if (sa >= r0 && sb <= r1) {
+        finish(sg, h, M, L, O);
+      } else {
+        float* dst = p.part_cta + ((size_t)blockIdx.x * 2 + (sa < r0 ? 0 : 1)) * kPgPart + h * kPartStride;
+        if (lane == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
+        *reinterpret_cast<float4*>(dst + 4 + 4 * lane) = O;
+      }
+    }
+  }
+
+  // ---- the segments at the range's ends that other CTAs share
+  __syncthreads();
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {
+    const int x = end == 0 ? r0 : r1 - 1;
+    const int row = batch_find(pre, x), items = row_of(row).items;
+    int rel;
+    const int head = div_small(x - pre[row], items, rel), s = row * hkv + head;
+    const int sa = x - rel, sb = sa + items;
+    if (sa >= r0 && sb <= r1) continue;      // finished here
+    if (end == 1 && sa <= r0) continue;      // one segment fills the range
+    if (tid == 0) {
+      const uint32_t mine = (uint32_t)(min(sb, r1) - max(sa, r0));
+      __threadfence();  // the block's partials (before the barrier) come before its ticket
+      const bool all = atomicAdd(&p.ticket[s], mine) + mine == (uint32_t)(sb - sa);
+      if (all) {
+        __threadfence();  // the others' partials are read after it
+        p.ticket[s] = 0u;
+      }
+      s_last = all;
+    }
+    const int ca = ctas.part_of(sa), cb = ctas.part_of(sb - 1);
+    __syncthreads();
+    const bool last = s_last != 0;
+    __syncthreads();
+    if (!last) continue;
+    // G heads, 16 / G warps each on every so-manieth CTA's partial
+    const int per = kPgWarps / G, h = warp % G, sub = warp / G;
+    auto part = [&](int c) {
+      return p.part_cta + ((size_t)c * 2 + (sa < ctas.begin(c) ? 0 : 1)) * kPgPart + h * kPartStride;
+    };
+    float* buf = reinterpret_cast<float*>(pa_smem) + warp * kPartStride;
+    if (sub < per) {
+      float M = kPaMin, L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+      constexpr int kAt = 8;  // partials whose loads are under way together
+      for (int c0 = ca + sub; c0 <= cb; c0 += kAt * per) {
+        float2 ml[kAt];
+        float4 v[kAt];
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+          const bool on = c0 + i * per <= cb;
+          const float* src = part(on ? c0 + i * per : c0);
+          ml[i] = on ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(kPaMin, 0.f);
+          v[i] = on ? __ldcg(reinterpret_cast<const float4*>(src + 4 + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float n = M;
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) n = fmaxf(n, ml[i].x);
+        const float fo = exp2f(M - n);
+        M = n;
+        L *= fo;
+        O.x *= fo;
+        O.y *= fo;
+        O.z *= fo;
+        O.w *= fo;
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+          const float f = exp2f(ml[i].x - M);
+          L = fmaf(ml[i].y, f, L);
+          O.x = fmaf(v[i].x, f, O.x);
+          O.y = fmaf(v[i].y, f, O.y);
+          O.z = fmaf(v[i].z, f, O.z);
+          O.w = fmaf(v[i].w, f, O.w);
+        }
       }
       if (lane == 0) {
         buf[0] = M;
@@ -723,7 +842,6 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       }
       finish(s, h, M, L, O);
     }
-    if (tid == 0) p.ticket[s] = 0u;
     __syncthreads();
   }
 }

@@ -81,11 +81,13 @@ class Ref:
                     + 2.0**-16 * ((s * code + z) @ a) + 2.0**-22 * 15 * 128 * a.max()
             e = scale * (e[seen] + 2.0**-16 * size) + 2.0**-20 * (1 + np.abs(x))
             # Errors of a weight: the logit's, fp16's rounding of the weight
-            # and of its product with the scale; 2^-39 of the largest weight
-            # is lost at the bottom of fp16, and its product with a scale
-            # 2^-40 (times the code's 15).
+            # and of its product with the scale.  The largest weight lies
+            # between 2^(sh - 5) and 2^sh, sh = 15 and less where value scales
+            # are 2 and more; 2^-25 is lost at the bottom of fp16, of a weight
+            # and of its product with a scale (times the code's 15).
             w = 2.0**-11
-            lost = 2.0**-39 * p.max()
+            top = 0 if not self.nq else np.floor(np.log2(max(float(self.c.v_scale[0, j].max()), 1.0)))
+            lost = 2.0**-(25 + 15 - top - 5) * p.max()
             ce = np.abs(v)
             if self.nq:
                 vs = np.repeat(self.c.v_scale[0, j].astype(float), 32, -1) * self.c.v_codes[0, j]
