@@ -7,8 +7,6 @@
 namespace jfa {
 
 constexpr int kPcThreads = 256;
-constexpr int kPcPitch = kD + 8;  // bf16 per staged row: 272 bytes, so that the 8 rows a
-                                  // fragment reads fall into different banks
 
 // ---------------------------------------------------------------------------
 // append
@@ -23,240 +21,400 @@ struct PagedAppendParams {
   int n_total, n_each;
 };
 
-// Code of x in a group of zero point z and scale s, both in fp32, inv = 1/s:
-// the rule's fp64 quotient (jfa_quant.cuh) wherever the fp32 one is too near
-// a border between two codes to decide.  The fp32 quotient's error is below
-// 3 * 2^-24 relative, 3e-6 at 15.
-__device__ __forceinline__ uint32_t code4(float x, float z, float s, float inv) {
-  const float r = (x - z) * inv;
-  const float t = rintf(r);
-  if (fabsf(r - t) > 0.49999f) return quant_code((double)x, (double)z, (double)s, 4);
-  return (uint32_t)fminf(fmaxf(t, 0.f), 15.f);
-}
-
-struct GroupParams {
-  float z, s, inv;
-};
-__device__ __forceinline__ GroupParams group_params(float mn, float mx, uint16_t& sb, uint16_t& zb) {
+// Scale and zero point of a group from its fp32 minimum and maximum (bf16
+// values), by the rule of jfa_quant.cuh.  The fp32 quotient is 2^-22 off at
+// most; where that leaves the scale's directed rounding open (a range that is
+// 15 times an fp16 number: every fifteenth), the smaller candidate is right if
+// 15 times it, exact in fp32, reaches the range; fp64 decides where the range
+// is not exact in fp32.
+__device__ __noinline__ uint16_t scale_fp64(float mn, float mx) {
+  uint16_t sb, zb;
   double z, s;
   quant_params((double)mn, (double)mx, 4, zb, sb, z, s);
+  return sb;
+}
+struct GroupParams {
+  float z, inv;  // zero point, 1 / scale (0 for scale 0: every code 0)
+  uint16_t sb, zb;
+};
+__device__ __forceinline__ GroupParams group_params(float mn, float mx) {
   GroupParams g;
-  g.z = (float)z;
-  g.s = (float)s;
-  g.inv = s > 0.0 ? 1.0f / g.s : 0.f;  // scale 0: every code 0
+  const __half zh = __float2half_rd(mn);
+  g.zb = __half_as_ushort(zh);
+  g.z = __half2float(zh);
+  const float d = mx - g.z, q = d * (1.f / 15.f);
+  const __half lo = __float2half_ru(q * (1.f - 0x1p-21f)), hi = __float2half_ru(q * (1.f + 0x1p-21f));
+  g.sb = __half_as_ushort(lo);
+  if (g.sb != __half_as_ushort(hi)) {
+    if (!(d + g.z == mx && mx - d == g.z)) g.sb = scale_fp64(mn, mx);
+    else if (15.f * __half2float(lo) < d) g.sb = __half_as_ushort(hi);
+  }
+  const float s = __half2float(__ushort_as_half(g.sb));
+  g.inv = s > 0.f ? 1.f / s : 0.f;
   return g;
 }
 
-// The rows of sequence `row` among the new ones: the first and how many.  A
-// range longer than its sequence is padded in front.
-__device__ __forceinline__ void new_rows(const PagedAppendParams& p, int row, int len, int& a, int& n) {
-  a = p.cu ? p.cu[row] : row * p.n_each;
-  n = p.cu ? p.cu[row + 1] - a : p.n_each;
-  if (n > len) {
-    a += n - len;
-    n = len;
-  }
+// Eight codes of a word: x[a][e][b] at bit 4 a + 16 e + 8 b, of the group [a][e].
+// t = 1.5 * 2^23 + round((x - z) / s): the sum of the shifted bit patterns less
+// that of 1.5 * 2^23's is the word.  The fp32 quotient's error is below 3e-6 at
+// 15; a word with one that near a border (or not a number) is formed again at
+// the end, by exact remainders.  bf16 numbers over an fp16 scale lie on a
+// border exactly about once in 900: each thread takes its own such words, one
+// in fourteen threads has one, so that a warp passes there once or twice.
+struct WordIn {
+  float x[2][2][2], z[2][2], inv[2][2];
+};
+__device__ __noinline__ uint32_t code_fp64(float x, float z, float s) {
+  return quant_code((double)x, (double)z, (double)s, 4);
 }
+// The remainder d - (c + 1/2) s at the border next to the quotient is exact,
+// and so is its sign, where d = x - z is (both ways of undoing it agree); else
+// the fp64 quotient decides.
+__device__ __forceinline__ uint32_t word_exact(const WordIn& in) {
+  uint32_t word = 0u;
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // the scale is the fp16 number nearest to 1 / inv
+      const float z = in.z[a][e], inv = in.inv[a][e], s = inv > 0.f ? __half2float(__float2half_rn(1.f / inv)) : 0.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float x = in.x[a][e][b], d = x - z, down = floorf(d * inv), rest = fmaf(-(down + 0.5f), s, d);
+        uint32_t c = (uint32_t)(int)down;
+        c += rest > 0.f || (rest == 0.f && (c & 1u)) ? 1u : 0u;
+        if (!(d + z == x && x - d == z && s > 0.f)) c = code_fp64(x, z, s);
+        word |= (c & 15u) << (4 * a + 16 * e + 8 * b);
+      }
+    }
+  return word;
+}
+__device__ __forceinline__ uint32_t quant_word(const WordIn& in, bool& near) {
+  constexpr float kRound = 12582912.f;
+  constexpr uint32_t kBits = 0x4B400000u;
+  uint32_t word = 0u;
+  near = false;
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float d = in.x[a][e][b] - in.z[a][e], t = fmaf(d, in.inv[a][e], kRound);
+        near |= !(fabsf(fmaf(d, in.inv[a][e], kRound - t)) <= 0.49999f);
+        word += __float_as_uint(t) << (4 * a + 16 * e + 8 * b);
+      }
+  return word - kBits * 0x11111111u;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t part(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// A CTA per (unit, KV head); a unit is one page of a row to be packed.  The
-// first unit of a row that gets tokens (there is one even when no page is
-// complete) also rewrites the row's tail, after it has read what it packs of
-// the old one; the later pages of the row hold new tokens only.
+constexpr int kApThreads = 128;
+
+// A CTA per (unit, KV head, keys or values); a unit is one page of a sequence
+// to be packed.  The first unit of a sequence that gets tokens (there is one
+// even when no page is complete) also rewrites the tail, after it has read
+// what it packs of the old one; the later pages hold new tokens only.
 //
+// The rows go from memory to registers to the record: a thread loads the
+// 16-byte chunks whose codes share words of the record (keys: chunks w and
+// w + 8 of tokens t and t + 8, twice; values: chunks 2 m, 2 m + 1, + 8, + 9 of
+// a token pair), so that shared memory carries only the key channels' ranges.
 // Memory traffic is the bound for prompts (512 B of rows in and 152 B of
 // record out per token and KV head); a decode step's append (one row a
-// sequence) is bound by its launch and two dependent loads.  The codes are
-// formed from fp32 quotients, eight to a 32-bit word of the record, each
-// thread storing 16 bytes of key and of value codes.
-__global__ void __launch_bounds__(kPcThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
-  __shared__ int pre[kMaxBatch + 1];
-  __shared__ int wsum[kMaxBatch / 32];
-  __shared__ __align__(16) uint16_t xk[kKG][kPcPitch];
-  __shared__ __align__(16) uint16_t xv[kKG][kPcPitch];
-  __shared__ float ks[kD], kz[kD], kinv[kD];
-  __shared__ float vs[kKG][4], vz[kKG][4], vinv[kKG][4];
-  __shared__ float2 mm[4][kD];
-  const int tid = threadIdx.x, h = blockIdx.y;
+// sequence) is bound by its launch and two dependent loads.
+__global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+  __shared__ int wsum[kApThreads / 32];
+  __shared__ int mine[5];  // row, unit of it, first new row, their number, length
+  __shared__ uint32_t rng[2][kApThreads / 32][kD / 2];  // key minima, maxima (channel pairs) by warp
+  // key zero point, 1 / scale; ten to a chunk of 8 channels against bank conflicts
+  __shared__ __align__(16) float2 zi[kD / 8 * 10];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+  const bool keys = blockIdx.z == 0;
   pdl_wait();
   // The attention that follows may become resident now.  Not before the wait:
   // a next kernel that reads earlier kernels' results ahead of its own wait
   // finds those complete.
   pdl_launch_dependents();
-  int units = 0;
-  if (tid < p.c.batch) {
-    const int len = checked_len(p.c.seq_lens[tid], p.c.max_pages, p.flag);
-    const int c0 = p.cu ? p.cu[tid] : 0, c1 = p.cu ? p.cu[tid + 1] : 0;
-    if (c0 < 0 || c1 < c0 || c1 > p.n_total) {
-      set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
-    } else {
-      int a, n_new;
-      new_rows(p, tid, len, a, n_new);
-      if (n_new > 0) units = max(1, (split_point(len) - split_point(len - n_new)) / kKG);
+  {
+    static_assert(kMaxBatch == 2 * kApThreads, "two sequences a thread");
+    int units[2] = {0, 0}, a[2] = {0, 0}, n_new[2] = {0, 0}, len[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // all loads first
+      const int row = 2 * tid + i;
+      if (row >= p.c.batch) continue;
+      len[i] = p.c.seq_lens[row];
+      a[i] = p.cu ? p.cu[row] : row * p.n_each;
+      n_new[i] = (p.cu ? p.cu[row + 1] : a[i] + p.n_each);  // (the range's end)
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (a[i] < 0 || n_new[i] < a[i] || n_new[i] > p.n_total) {
+        set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
+        continue;
+      }
+      len[i] = checked_len(len[i], p.c.max_pages, p.flag);
+      n_new[i] -= a[i];
+      if (n_new[i] > len[i]) {  // a range longer than its sequence is padded in front
+        a[i] += n_new[i] - len[i];
+        n_new[i] = len[i];
+      }
+      if (n_new[i] > 0) units[i] = max(1, (split_point(len[i]) - split_point(len[i] - n_new[i])) / kKG);
+    }
+    // which sequence has this CTA's unit: prefix sums over the sequences
+    int s = units[0] + units[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane == 31) wsum[warp] = s;
+    if (tid == 0) mine[0] = -1;
+    __syncthreads();
+    int at = s - units[0] - units[1];
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    const int x = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (x >= at && x < at + units[i]) {
+        mine[0] = 2 * tid + i;
+        mine[1] = x - at;
+        mine[2] = a[i];
+        mine[3] = n_new[i];
+        mine[4] = len[i];
+      }
+      at += units[i];
+    }
+    __syncthreads();
   }
-  batch_prefix(units, pre, wsum);
-  const int x = blockIdx.x;
-  if (x >= pre[kMaxBatch]) return;
-  const int row = batch_find(pre, x), j = x - pre[row];
-  const int n1 = p.c.seq_lens[row];
-  int a, n_new;
-  new_rows(p, row, n1, a, n_new);
-  const int n0 = n1 - n_new;
-  const int nq0 = split_point(n0), nq1 = split_point(n1);
+  const int row = mine[0], j = mine[1], n_new = mine[3], n1 = mine[4];
+  if (row < 0) return;
+  const int n0 = n1 - n_new, nq0 = split_point(n0), nq1 = split_point(n1);
   const size_t seg = (size_t)row * p.c.num_kv_heads + h;
-  uint8_t* tail[2] = {reinterpret_cast<uint8_t*>(p.c.tail_k) + seg * kPgTailBytes,
-                      reinterpret_cast<uint8_t*>(p.c.tail_v) + seg * kPgTailBytes};
-  const uint16_t* fresh[2] = {p.k_new + (int64_t)a * p.k_tok + h * p.k_head,
-                              p.v_new + (int64_t)a * p.v_tok + h * p.v_head};
-  const int64_t tok[2] = {p.k_tok, p.v_tok};
+  uint8_t* tail = reinterpret_cast<uint8_t*>(keys ? p.c.tail_k : p.c.tail_v) + seg * kPgTailBytes;
+  const int64_t tok = keys ? p.k_tok : p.v_tok;
+  const uint16_t* fresh = (keys ? p.k_new + h * p.k_head : p.v_new + h * p.v_head) + (int64_t)mine[2] * tok;
 
   if (nq1 > nq0) {
     const int g = nq0 / kKG + j, t0 = g * kKG;
     const int page = p.c.table[(size_t)row * p.c.max_pages + g];
     const bool page_ok = page >= 0 && page < p.c.n_pages;
     if (!page_ok && tid == 0) set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
-    // the group's rows: from the old tail below n0, else new
-    {
-      uint4 w[2][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = (tid >> 4) + 16 * i, ch = tid & 15, tau = t0 + t;
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          w[m][i] = tau < n0 ? *reinterpret_cast<const uint4*>(tail[m] + tail_chunk(tau - nq0, ch))
-                             : *reinterpret_cast<const uint4*>(fresh[m] + (int64_t)(tau - n0) * tok[m] + 8 * ch);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = (tid >> 4) + 16 * i, ch = tid & 15;
-        *reinterpret_cast<uint4*>(&xk[t][8 * ch]) = w[0][i];
-        *reinterpret_cast<uint4*>(&xv[t][8 * ch]) = w[1][i];
-      }
-    }
-    __syncthreads();
-    // keys: range of a channel pair over 16 tokens; values: of a (token, 32 channels)
-    {
-      const int cp = tid & 63, q = tid >> 6;
-      float2 lo = make_float2(INFINITY, INFINITY), hi = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(&xk[16 * q + t][2 * cp]);
-        const float e0 = __uint_as_float(w << 16), e1 = __uint_as_float(w & 0xFFFF0000u);
-        lo.x = fminf(lo.x, e0);
-        hi.x = fmaxf(hi.x, e0);
-        lo.y = fminf(lo.y, e1);
-        hi.y = fmaxf(hi.y, e1);
-      }
-      mm[q][2 * cp] = make_float2(lo.x, hi.x);
-      mm[q][2 * cp + 1] = make_float2(lo.y, hi.y);
-    }
-    bool bad = false;
     uint8_t* rec = static_cast<uint8_t*>(p.c.pages) +
                    ((size_t)(page_ok ? page : 0) * p.c.num_kv_heads + h) * kPgRec;
-    {
-      const int t = tid >> 2, jj = tid & 3;
-      float lo = INFINITY, hi = -INFINITY;
+    // chunk ch of the group's token t: from the old tail below n0, else new
+    auto load = [&](int t, int ch) {
+      const int tau = t0 + t;
+      const void* at = tau < n0 ? static_cast<const void*>(tail + tail_chunk(tau - nq0, ch))
+                                : static_cast<const void*>(fresh + (int64_t)(tau - n0) * tok + 8 * ch);
+      return *static_cast<const uint4*>(at);
+    };
+    auto load_pair = [&](int t, int ch, int i) {  // its channels 2 i, 2 i + 1
+      const int tau = t0 + t;
+      const void* at = tau < n0 ? static_cast<const void*>(tail + tail_chunk(tau - nq0, ch) + 4 * i)
+                                : static_cast<const void*>(fresh + (int64_t)(tau - n0) * tok + 8 * ch + 2 * i);
+      return *static_cast<const uint32_t*>(at);
+    };
+    bool bad = false;
+    if (keys) {
+      // lane (g4, w), pass k: tokens t = 16 mt + gid and t + 8 with 8 mt + gid = 16 k + 4 warp + g4
+      const int w = lane & 7, q0 = 4 * warp + (lane >> 3);
+      uint4 x[2][2][2];  // [pass][r][chunk w, w + 8]
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 w = *reinterpret_cast<const uint4*>(&xv[t][32 * jj + 8 * i]);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      for (int k = 0; k < 2; ++k) {
+        const int q = q0 + 16 * k, t = (q >> 3) * 16 + (q & 7);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float e0 = __uint_as_float(ww[e] << 16), e1 = __uint_as_float(ww[e] & 0xFFFF0000u);
-          lo = fminf(lo, fminf(e0, e1));
-          hi = fmaxf(hi, fmaxf(e0, e1));
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) x[k][r][c] = load(t + 8 * r, w + 8 * c);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t lo = part(x[0][0][c], i), hi = lo;
+#pragma unroll
+          for (int k = 1; k < 4; ++k) {
+            lo = bmin2(lo, part(x[k >> 1][k & 1][c], i));
+            hi = bmax2(hi, part(x[k >> 1][k & 1][c], i));
+          }
+#pragma unroll
+          for (int o = 8; o < 32; o <<= 1) {
+            lo = bmin2(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+            hi = bmax2(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+          }
+          if (lane < 8) {
+            rng[0][warp][4 * (w + 8 * c) + i] = lo;
+            rng[1][warp][4 * (w + 8 * c) + i] = hi;
+          }
+        }
+      __syncthreads();
+      {
+        uint32_t lo = rng[0][0][tid >> 1], hi = rng[1][0][tid >> 1];
+#pragma unroll
+        for (int i = 1; i < kApThreads / 32; ++i) {
+          lo = bmin2(lo, rng[0][i][tid >> 1]);
+          hi = bmax2(hi, rng[1][i][tid >> 1]);
+        }
+        const GroupParams gp = group_params(tid & 1 ? bf_hi(lo) : bf_lo(lo), tid & 1 ? bf_hi(hi) : bf_lo(hi));
+        bad |= !finite_h(gp.sb) || !finite_h(gp.zb);
+        zi[(tid >> 3) * 10 + (tid & 7)] = make_float2(gp.z, gp.inv);
+        if (page_ok) {
+          *reinterpret_cast<uint16_t*>(rec + off_ks() + ks_scale_off(tid)) = gp.sb;
+          *reinterpret_cast<uint16_t*>(rec + off_ks() + ks_zero_off(tid)) = gp.zb;
         }
       }
-      uint16_t sb, zb;
-      const GroupParams gp = group_params(lo, hi, sb, zb);
-      bad |= !finite_h(sb) || !finite_h(zb);
-      vs[t][jj] = gp.s;
-      vz[t][jj] = gp.z;
-      vinv[t][jj] = gp.inv;
-      if (page_ok) {
-        *reinterpret_cast<uint16_t*>(rec + off_vs(4) + vs_scale_off(t, jj)) = sb;
-        *reinterpret_cast<uint16_t*>(rec + off_vs(4) + vs_zero_off(t, jj)) = zb;
-      }
-    }
-    __syncthreads();
-    if (tid < kD) {
-      float lo = mm[0][tid].x, hi = mm[0][tid].y;
+      __syncthreads();
+      // a word's inputs: the channel pair's numbers of chunks w, w + 8 (c) and tokens t, t + 8 (r)
+      auto key_word = [&](const float4 par[2], uint32_t v00, uint32_t v01, uint32_t v10, uint32_t v11) {
+        const uint32_t v[2][2] = {{v00, v01}, {v10, v11}};
+        WordIn in;
 #pragma unroll
-      for (int q = 1; q < 4; ++q) {
-        lo = fminf(lo, mm[q][tid].x);
-        hi = fmaxf(hi, mm[q][tid].y);
+        for (int c = 0; c < 2; ++c) {
+          in.z[c][0] = par[c].x, in.inv[c][0] = par[c].y, in.z[c][1] = par[c].z, in.inv[c][1] = par[c].w;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            in.x[c][0][r] = bf_lo(v[c][r]);
+            in.x[c][1][r] = bf_hi(v[c][r]);
+          }
+        }
+        return in;
+      };
+      auto word_at = [&](int i, int k) {
+        const int q = q0 + 16 * k;
+        return reinterpret_cast<uint32_t*>(rec + off_kc() + (q >> 3) * 1024 + ((q & 7) * 4 + i) * 32 + 4 * w);
+      };
+      uint32_t again = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // channels 2 i, 2 i + 1 of the chunks: word w of lane 4 gid + i
+        float4 par[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) par[c] = *reinterpret_cast<const float4*>(&zi[(w + 8 * c) * 10 + 2 * i]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          bool near;
+          const uint32_t word = quant_word(key_word(par, part(x[k][0][0], i), part(x[k][1][0], i), part(x[k][0][1], i),
+                                                    part(x[k][1][1], i)), near);
+          again |= (uint32_t)near << (2 * i + k);
+          if (page_ok) *word_at(i, k) = word;
+        }
       }
-      uint16_t sb, zb;
-      const GroupParams gp = group_params(lo, hi, sb, zb);
-      bad |= !finite_h(sb) || !finite_h(zb);
-      ks[tid] = gp.s;
-      kz[tid] = gp.z;
-      kinv[tid] = gp.inv;
-      if (page_ok) {
-        *reinterpret_cast<uint16_t*>(rec + off_ks() + ks_scale_off(tid)) = sb;
-        *reinterpret_cast<uint16_t*>(rec + off_ks() + ks_zero_off(tid)) = zb;
+      for (; again && page_ok; again &= again - 1) {
+        const int i = (__ffs(again) - 1) >> 1, k = (__ffs(again) - 1) & 1, q = q0 + 16 * k, t = (q >> 3) * 16 + (q & 7);
+        float4 par[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) par[c] = *reinterpret_cast<const float4*>(&zi[(w + 8 * c) * 10 + 2 * i]);
+        *word_at(i, k) = word_exact(key_word(par, load_pair(t, w, i), load_pair(t + 8, w, i), load_pair(t, w + 8, i),
+                                             load_pair(t + 8, w + 8, i)));
+      }
+    } else {
+      // lane (hi8, m, tig): tokens t, t + 1 with t = 16 warp + 8 hi8 + 2 tig
+      const int tig = lane & 3, m = (lane >> 2) & 3, hi8 = lane >> 4, t = 16 * warp + 8 * hi8 + 2 * tig;
+      uint4 x[2][2][2];  // [token][32-channel group (m >> 1) + 2 hs][chunk 2 m + 8 hs, next]
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int hs = 0; hs < 2; ++hs)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) x[e][hs][c] = load(t + e, 2 * m + 8 * hs + c);
+      // ranges of the thread's 16 channels; the group's other 16 are lane ^ 4's
+      float mn[2][2], mx[2][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int hs = 0; hs < 2; ++hs) {
+          uint32_t lo = x[e][hs][0].x, hi = lo;
+#pragma unroll
+          for (int i = 1; i < 8; ++i) {
+            lo = bmin2(lo, part(x[e][hs][i >> 2], i & 3));
+            hi = bmax2(hi, part(x[e][hs][i >> 2], i & 3));
+          }
+          lo = bmin2(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 4));
+          hi = bmax2(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, 4));
+          mn[e][hs] = fminf(bf_lo(lo), bf_hi(lo));
+          mx[e][hs] = fmaxf(bf_lo(hi), bf_hi(hi));
+        }
+      // even m: the first token's two groups, odd m: the second's
+      const bool odd = m & 1;
+      float z[2][2], inv[2][2];
+#pragma unroll
+      for (int hs = 0; hs < 2; ++hs) {
+        const GroupParams gp = group_params(odd ? mn[1][hs] : mn[0][hs], odd ? mx[1][hs] : mx[0][hs]);
+        bad |= !finite_h(gp.sb) || !finite_h(gp.zb);
+        if (page_ok) {
+          uint8_t* at = rec + off_vs(4) + vs_scale_off(t + odd, (m >> 1) + 2 * hs);
+          *reinterpret_cast<uint16_t*>(at) = gp.sb;
+          *reinterpret_cast<uint16_t*>(at + 512) = gp.zb;
+        }
+        const float oz = __shfl_xor_sync(0xFFFFFFFFu, gp.z, 4), oi = __shfl_xor_sync(0xFFFFFFFFu, gp.inv, 4);
+        z[0][hs] = odd ? oz : gp.z;
+        z[1][hs] = odd ? gp.z : oz;
+        inv[0][hs] = odd ? oi : gp.inv;
+        inv[1][hs] = odd ? gp.inv : oi;
+      }
+      const int w8 = 2 * m + hi8;
+      uint8_t* at = rec + off_vc(4) + (2 * warp + (w8 >> 2)) * 512 + tig * 16 + 4 * (w8 & 3);
+      // a word's inputs: the lower or upper channel of v [token][32-channel group][chunk]
+      auto value_word = [&](const uint32_t v[2][2][2], bool up) {
+        WordIn in;
+#pragma unroll
+        for (int hs = 0; hs < 2; ++hs)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            in.z[hs][e] = z[e][hs];
+            in.inv[hs][e] = inv[e][hs];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) in.x[hs][e][c] = up ? bf_hi(v[e][hs][c]) : bf_lo(v[e][hs][c]);
+          }
+        return in;
+      };
+      uint32_t again = 0u;
+#pragma unroll
+      for (int gid = 0; gid < 8; ++gid) {  // channel gid of the chunks
+        uint32_t v[2][2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int hs = 0; hs < 2; ++hs)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) v[e][hs][c] = part(x[e][hs][c], gid >> 1);
+        bool near;
+        const uint32_t word = quant_word(value_word(v, gid & 1), near);
+        again |= (uint32_t)near << gid;
+        if (page_ok) *reinterpret_cast<uint32_t*>(at + gid * 64) = word;
+      }
+      for (; again && page_ok; again &= again - 1) {
+        const int gid = __ffs(again) - 1;
+        uint32_t v[2][2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int hs = 0; hs < 2; ++hs)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) v[e][hs][c] = load_pair(t + e, 2 * m + 8 * hs + c, gid >> 1);
+        *reinterpret_cast<uint32_t*>(at + gid * 64) = word_exact(value_word(v, gid & 1));
       }
     }
     if (bad) set_flag(p.flag, JFA_DEVERR_NONFINITE_QUANT);
-    __syncthreads();
-    // codes: a thread forms four consecutive words (16 bytes) of each section
-    // (kc_bits and vc_loc give the places)
-    {
-      const int mt = tid >> 6, lane = (tid >> 1) & 31, w0 = (tid & 1) * 4, gid = lane >> 2, tig = lane & 3;
-      uint32_t word[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int w = w0 + i;
-        uint32_t out = 0u;
-#pragma unroll
-        for (int hs = 0; hs < 2; ++hs) {  // slots w and w + 8: channels 64 apart
-          const int c = 16 * (w >> 1) + 2 * tig + 8 * (w & 1) + 64 * hs;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t pr = *reinterpret_cast<const uint32_t*>(&xk[16 * mt + gid + 8 * r][c]);
-            out |= code4(__uint_as_float(pr << 16), kz[c], ks[c], kinv[c]) << (4 * hs + 8 * r);
-            out |= code4(__uint_as_float(pr & 0xFFFF0000u), kz[c + 1], ks[c + 1], kinv[c + 1])
-                   << (4 * hs + 8 * r + 16);
-          }
-        }
-        word[i] = out;
-      }
-      if (page_ok)
-        *reinterpret_cast<uint4*>(rec + off_kc() + tid * 16) = make_uint4(word[0], word[1], word[2], word[3]);
-    }
-    {
-      const int kk = tid >> 6, half = (tid >> 5) & 1, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
-      uint32_t word[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int w8 = 4 * half + i, hi8 = w8 & 1;
-        uint32_t out = 0u;
-#pragma unroll
-        for (int hs = 0; hs < 2; ++hs) {  // m-tiles w8 / 2 and w8 / 2 + 4
-          const int mt = (w8 >> 1) + 4 * hs, jj = mt >> 1;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = 16 * kk + 2 * tig + 8 * hi8 + e;
-#pragma unroll
-            for (int chi = 0; chi < 2; ++chi)
-              out |= code4(bf(xv[t][16 * mt + gid + 8 * chi]), vz[t][jj], vs[t][jj], vinv[t][jj])
-                     << (4 * hs + 8 * chi + 16 * e);
-          }
-        }
-        word[i] = out;
-      }
-      if (page_ok)
-        *reinterpret_cast<uint4*>(rec + off_vc(4) + tid * 16) = make_uint4(word[0], word[1], word[2], word[3]);
-    }
   }
   // the new tail: after a packed page it restarts at nq1, all of it new
   // (slots past it keep what they held)
   if (j == 0) {
+    if (nq1 > nq0) __syncthreads();  // the old tail has been read
     const int from = nq1 > nq0 ? nq1 : n0;
-    for (int i = tid; i < (n1 - from) * 32; i += kPcThreads) {
-      const int m = i & 1, ch = (i >> 1) & 15, tau = from + (i >> 5);
-      *reinterpret_cast<uint4*>(tail[m] + tail_chunk(tau - nq1, ch)) =
-          *reinterpret_cast<const uint4*>(fresh[m] + (int64_t)(tau - n0) * tok[m] + 8 * ch);
+    for (int i = tid; i < (n1 - from) * 16; i += kApThreads) {
+      const int ch = i & 15, tau = from + (i >> 4);
+      *reinterpret_cast<uint4*>(tail + tail_chunk(tau - nq1, ch)) =
+          *reinterpret_cast<const uint4*>(fresh + (int64_t)(tau - n0) * tok + 8 * ch);
     }
   }
 }
@@ -278,7 +436,7 @@ int launch_paged_append(const jfa_paged& c, const uint16_t* k_new, int64_t k_tok
   p.n_each = n_total / c.batch;
   // a row of n tokens packs at most n / 64 pages beside its first unit
   const int rows = c.batch < n_total ? c.batch : n_total;
-  return launch_pdl(paged_append_kernel, dim3(rows + n_total / kKG, c.num_kv_heads), dim3(kPcThreads), 0, st, p) ==
+  return launch_pdl(paged_append_kernel, dim3(rows + n_total / kKG, c.num_kv_heads, 2), dim3(kApThreads), 0, st, p) ==
                  cudaSuccess
              ? JFA_OK
              : JFA_ERR_CUDA;
@@ -302,48 +460,96 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// A CTA per (64-token group of a row's range, KV head): the record through
-// shared memory (or the tail's rows), each half warp writing whole 256-byte
-// rows.  HBM-bound: 152 B in and 512 B out per token and KV head.
-__global__ void __launch_bounds__(kPcThreads) paged_gather_kernel(const __grid_constant__ PagedGatherParams p) {
-  __shared__ int pre[kMaxBatch + 1];
-  __shared__ int wsum[kMaxBatch / 32];
-  __shared__ __align__(16) uint8_t rec[kPgRec];
-  const int tid = threadIdx.x, h = blockIdx.y;
+// Eight codes of a word, shifted so that a byte of it holds the codes of two
+// scales: bits 0-3 with scale s, 4-7 with 16 s (given as s / 16, exact).
+__device__ __forceinline__ float code_value(uint32_t byte, int hs, float s, float z) {
+  const float f = __uint_as_float((byte & (15u << (4 * hs))) | 0x4B000000u) - 8388608.f;  // 2^23 + code 2^(4 hs)
+  return fmaf(f, s, z);
+}
+// 32 consecutive bytes of a row
+__device__ __forceinline__ void store32(uint16_t* o, const uint32_t* w) {
+  if ((reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+constexpr int kGtThreads = 128;
+
+// A CTA per (64-token group of a sequence's range, KV head, keys or values).
+// The record's words go from memory to registers to whole rows, by the same
+// shares as in the append: a thread's words hold the codes of whole 16-byte
+// chunks (keys: chunks w and w + 8 of tokens t and t + 8, twice; values: a
+// token pair's chunks 2 m, 2 m + 1, + 8, + 9), so nothing passes through shared
+// memory and all loads are under way together.  HBM-bound: 152 B in and 512 B
+// out per token and KV head.
+__global__ void __launch_bounds__(kGtThreads) paged_gather_kernel(const __grid_constant__ PagedGatherParams p) {
+  __shared__ int wsum[kGtThreads / 32];
+  __shared__ int mine[6];  // row, group of its range, first output row, their number, first token, length
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+  const bool keys = blockIdx.z == 0;
   pdl_wait();
-  int units = 0;
-  if (tid < p.c.batch) {
-    const int a = p.cu[tid], cnt = p.cu[tid + 1] - a, s = p.start ? p.start[tid] : 0;
-    if (cnt != 0) {
-      const int n = checked_len(p.c.seq_lens[tid], p.c.max_pages, p.flag);
-      if (a < 0 || cnt < 0 || a > p.n_total - cnt || s < 0 || s > n - cnt)
+  {
+    static_assert(kMaxBatch == 2 * kGtThreads, "two sequences a thread");
+    int units[2] = {0, 0}, a[2], cnt[2], from[2], len[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 2 * tid + i;
+      if (row >= p.c.batch) continue;
+      a[i] = p.cu[row];
+      cnt[i] = p.cu[row + 1] - a[i];
+      from[i] = p.start ? p.start[row] : 0;
+      if (cnt[i] == 0) continue;
+      len[i] = checked_len(p.c.seq_lens[row], p.c.max_pages, p.flag);
+      if (a[i] < 0 || cnt[i] < 0 || a[i] > p.n_total - cnt[i] || from[i] < 0 || from[i] > len[i] - cnt[i])
         set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
       else
-        units = (s + cnt - 1) / kKG - s / kKG + 1;
+        units[i] = (from[i] + cnt[i] - 1) / kKG - from[i] / kKG + 1;
     }
+    // which sequence has this CTA's unit: prefix sums over the sequences
+    int s = units[0] + units[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane == 31) wsum[warp] = s;
+    if (tid == 0) mine[0] = -1;
+    __syncthreads();
+    int at = s - units[0] - units[1];
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    const int x = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (x >= at && x < at + units[i]) {
+        mine[0] = 2 * tid + i;
+        mine[1] = x - at;
+        mine[2] = a[i];
+        mine[3] = cnt[i];
+        mine[4] = from[i];
+        mine[5] = len[i];
+      }
+      at += units[i];
+    }
+    __syncthreads();
   }
-  batch_prefix(units, pre, wsum);
-  const int x = blockIdx.x;
-  if (x >= pre[kMaxBatch]) return;
-  const int row = batch_find(pre, x);
-  const int a = p.cu[row], cnt = p.cu[row + 1] - a, s = p.start ? p.start[row] : 0;
-  const int n = p.c.seq_lens[row], nq = split_point(n);
-  const int g = s / kKG + x - pre[row], t0 = g * kKG;
+  const int row = mine[0], a = mine[2], cnt = mine[3], s = mine[4], nq = split_point(mine[5]);
+  if (row < 0) return;
+  const int g = s / kKG + mine[1], t0 = g * kKG;
   const int lo = max(s, t0) - t0, hi = min(s + cnt, t0 + kKG) - t0;  // tokens of the group to write
-  const int ch = tid & 15;
   const int64_t pitch = (int64_t)p.c.num_kv_heads * kD;
-  const int64_t first = ((int64_t)a + t0 - s) * pitch + (int64_t)h * kD + 8 * ch;  // of token t0 (may lie before the rows)
-  uint16_t* ko = p.k_out + first;
-  uint16_t* vo = p.v_out + first;
+  // of token t0 (may lie before the rows)
+  uint16_t* out = (keys ? p.k_out : p.v_out) + ((int64_t)a + t0 - s) * pitch + (int64_t)h * kD;
   if (t0 >= nq) {
-    const size_t seg = (size_t)row * p.c.num_kv_heads + h;
-    const uint8_t* tk = reinterpret_cast<const uint8_t*>(p.c.tail_k) + seg * kPgTailBytes;
-    const uint8_t* tv = reinterpret_cast<const uint8_t*>(p.c.tail_v) + seg * kPgTailBytes;
-    for (int t = tid >> 4; t < hi; t += 16) {
-      if (t < lo) continue;
-      *reinterpret_cast<uint4*>(ko + t * pitch) = *reinterpret_cast<const uint4*>(tk + tail_chunk(t, ch));
-      *reinterpret_cast<uint4*>(vo + t * pitch) = *reinterpret_cast<const uint4*>(tv + tail_chunk(t, ch));
-    }
+    const uint8_t* tail = reinterpret_cast<const uint8_t*>(keys ? p.c.tail_k : p.c.tail_v) +
+                          ((size_t)row * p.c.num_kv_heads + h) * kPgTailBytes;
+    for (int i = lo * 16 + tid; i < hi * 16; i += kGtThreads)
+      *reinterpret_cast<uint4*>(out + (i >> 4) * pitch + 8 * (i & 15)) =
+          *reinterpret_cast<const uint4*>(tail + tail_chunk(i >> 4, i & 15));
     return;
   }
   const int page = p.c.table[(size_t)row * p.c.max_pages + g];
@@ -351,54 +557,73 @@ __global__ void __launch_bounds__(kPcThreads) paged_gather_kernel(const __grid_c
     if (tid == 0) set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
     return;
   }
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.c.pages) +
-                                                    ((size_t)page * p.c.num_kv_heads + h) * kPgRec);
-  for (int i = tid; i < kPgRec / 16; i += kPcThreads) reinterpret_cast<uint4*>(rec)[i] = __ldg(src + i);
-  __syncthreads();
-  // keys: channels 8 ch .. + 7 are pair slot ch of the four lanes tig
-  float s8[8], z8[8];
+  const uint8_t* rec = static_cast<const uint8_t*>(p.c.pages) + ((size_t)page * p.c.num_kv_heads + h) * kPgRec;
+  auto word = [&](int at) { return __ldg(reinterpret_cast<const uint32_t*>(rec + at)); };
+  auto half2f = [](uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); };
+  if (keys) {
+    const int w = lane & 7, q0 = 4 * warp + (lane >> 3);
+    uint32_t code[2][4], sc[2][4], zp[2][4];
 #pragma unroll
-  for (int tig = 0; tig < 4; ++tig) {
-    const int o = (ch >> 2) * 64 + tig * 16 + (ch & 3) * 4;
-    const float2 sv = __half22float2(*reinterpret_cast<const __half2*>(rec + o));
-    const float2 zv = __half22float2(*reinterpret_cast<const __half2*>(rec + 256 + o));
-    s8[2 * tig] = sv.x;
-    s8[2 * tig + 1] = sv.y;
-    z8[2 * tig] = zv.x;
-    z8[2 * tig + 1] = zv.y;
-  }
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = (tid >> 4) + 16 * i, gid = t & 7, r = (t >> 3) & 1;
-    if (t < lo || t >= hi) continue;
-    {
-      const int sh = 4 * (ch >> 3) + 8 * r;
-      uint32_t o[4];
+      for (int k = 0; k < 2; ++k) code[k][i] = word(off_kc() + ((q0 + 16 * k) >> 3) * 1024 + ((q0 & 7) * 4 + i) * 32 + 4 * w);
 #pragma unroll
-      for (int tig = 0; tig < 4; ++tig) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + off_kc() + i * 1024 + (gid * 4 + tig) * 32 +
-                                                              4 * (ch & 7)) >> sh;
-        o[tig] = pack_bf2(fmaf((float)(w & 15u), s8[2 * tig], z8[2 * tig]),
-                          fmaf((float)((w >> 16) & 15u), s8[2 * tig + 1], z8[2 * tig + 1]));
+      for (int c = 0; c < 2; ++c) {  // chunk w + 8 c: pair slot w + 8 c of lane i
+        const int at = ((w >> 2) + 2 * c) * 64 + i * 16 + (w & 3) * 4;
+        sc[c][i] = word(at);
+        zp[c][i] = word(256 + at);
       }
-      *reinterpret_cast<uint4*>(ko + t * pitch) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    {
-      const int mt = ch >> 1, hi8 = (t >> 3) & 1, tig = (t & 7) >> 1, e = t & 1, w8 = 2 * (mt & 3) + hi8;
-      const int sh = 4 * (mt >> 2) + 8 * (ch & 1) + 16 * e;
-      const int so = off_vs(4) + vs_scale_off(t, ch >> 2);
-      const float s = __half2float(*reinterpret_cast<const __half*>(rec + so));
-      const float z = __half2float(*reinterpret_cast<const __half*>(rec + so + 512));
-      const uint8_t* wp = rec + off_vc(4) + (2 * i + (w8 >> 2)) * 512 + tig * 16 + 4 * (w8 & 3);
-      uint32_t o[4];
 #pragma unroll
-      for (int gp = 0; gp < 4; ++gp) {
-        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wp + (2 * gp) * 64) >> sh;
-        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wp + (2 * gp + 1) * 64) >> sh;
-        o[gp] = pack_bf2(fmaf((float)(w0 & 15u), s, z), fmaf((float)(w1 & 15u), s, z));
+    for (int c = 0; c < 2; ++c) {
+      float2 s2[4], z2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s2[i] = half2f(sc[c][i]);
+        z2[i] = half2f(zp[c][i]);
+        if (c) s2[i] = make_float2(s2[i].x * 0.0625f, s2[i].y * 0.0625f);
       }
-      *reinterpret_cast<uint4*>(vo + t * pitch) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int q = q0 + 16 * k, t = (q >> 3) * 16 + (q & 7) + 8 * r;
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = pack_bf2(code_value(code[k][i] >> (8 * r), c, s2[i].x, z2[i].x),
+                            code_value(code[k][i] >> (8 * r + 16), c, s2[i].y, z2[i].y));
+          if (t >= lo && t < hi)
+            *reinterpret_cast<uint4*>(out + t * pitch + 8 * (w + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
+  } else {
+    const int tig = lane & 3, m = (lane >> 2) & 3, hi8 = lane >> 4, t = 16 * warp + 8 * hi8 + 2 * tig, w8 = 2 * m + hi8;
+    uint32_t code[8], sc[2], zp[2];
+#pragma unroll
+    for (int hs = 0; hs < 2; ++hs) {
+      const int at = off_vs(4) + vs_scale_off(t, (m >> 1) + 2 * hs);  // of both tokens
+      sc[hs] = word(at);
+      zp[hs] = word(at + 512);
+    }
+#pragma unroll
+    for (int gid = 0; gid < 8; ++gid)
+      code[gid] = word(off_vc(4) + (2 * warp + (w8 >> 2)) * 512 + (gid * 4 + tig) * 16 + 4 * (w8 & 3));
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int hs = 0; hs < 2; ++hs) {
+        const float2 s2 = half2f(sc[hs]), z2 = half2f(zp[hs]);
+        const float sv = (e ? s2.y : s2.x) * (hs ? 0.0625f : 1.f), zv = e ? z2.y : z2.x;
+        uint32_t o[8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[4 * c + i] = pack_bf2(code_value(code[2 * i] >> (8 * c + 16 * e), hs, sv, zv),
+                                    code_value(code[2 * i + 1] >> (8 * c + 16 * e), hs, sv, zv));
+        if (t + e >= lo && t + e < hi) store32(out + (t + e) * pitch + 16 * m + 64 * hs, o);
+      }
   }
 }
 
@@ -415,7 +640,7 @@ int launch_paged_gather(const jfa_paged& c, const int32_t* cu, const int32_t* st
   // a range of n > 0 tokens touches at most n / 64 + 2 groups (n groups when n < 2)
   const long long rows = c.batch < n_total ? c.batch : n_total;
   const unsigned grid = (unsigned)(n_total / kKG + 2 * rows);
-  return launch_pdl(paged_gather_kernel, dim3(grid, c.num_kv_heads), dim3(kPcThreads), 0, st, p) == cudaSuccess
+  return launch_pdl(paged_gather_kernel, dim3(grid, c.num_kv_heads, 2), dim3(kGtThreads), 0, st, p) == cudaSuccess
              ? JFA_OK
              : JFA_ERR_CUDA;
 }
