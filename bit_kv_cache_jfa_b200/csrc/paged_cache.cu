@@ -141,10 +141,6 @@ __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
   const bool keys = blockIdx.z == 0;
   pdl_wait();
-  // The attention that follows may become resident now.  Not before the wait:
-  // a next kernel that reads earlier kernels' results ahead of its own wait
-  // finds those complete.
-  pdl_launch_dependents();
   {
     static_assert(kMaxBatch == 2 * kApThreads, "two sequences a thread");
     int units[2] = {0, 0}, a[2] = {0, 0}, n_new[2] = {0, 0}, len[2] = {0, 0};

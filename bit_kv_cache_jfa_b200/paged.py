@@ -180,14 +180,18 @@ def qk_norm_rope(q, k, positions, plan: RotaryPlan, q_weight=None, k_weight=None
     kw = None if k_weight is None else _weight(k_weight, dev, where, "k_weight")
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        qop, qo_tok, qo_head = q_out.data_ptr(), h * 128, 128
     elif q_out.shape != qs:
         _refuse(where, "outputs must have their inputs' shapes")
+    else:
+        qop, qo_tok, qo_head = _rows(q_out, h, dev, where, "q_out")
     if k_out is None:
         k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        kop, ko_tok, ko_head = k_out.data_ptr(), hkv * 128, 128
     elif k_out.shape != ks:
         _refuse(where, "outputs must have their inputs' shapes")
-    qop, qo_tok, qo_head = _rows(q_out, h, dev, where, "q_out")
-    kop, ko_tok, ko_head = _rows(k_out, hkv, dev, where, "k_out")
+    else:
+        kop, ko_tok, ko_head = _rows(k_out, hkv, dev, where, "k_out")
     r = Rope(t, h, hkv, plan.rotary_dim, plan.interleaved, wide, eps, plan.amplitude, qp, kp, qop, kop, q_tok,
              q_head, k_tok, k_head, qo_tok, qo_head, ko_tok, ko_head, qw, kw, positions.data_ptr(),
              plan.freq_ptr)
