@@ -43,9 +43,10 @@ constexpr int kPaK = 512 + 4096;   // key scales, zero points and codes
 constexpr int kPaV = 1024 + 4096;  // the same of the values
 // Per warp two key buffers and one value buffer: while the values of a group
 // are used the next keys have arrived, and while keys are used the values
-// arrive.  16 warps hold about 150 KB in flight per SM.
-constexpr int kPaKBuf = 2;
-constexpr int kPaWarpBytes = kPaKBuf * kPaK + kPaV;
+// arrive.  A third key buffer gains nothing (a warp does not wait for copies
+// once the first have come, about 130 of its 4500 cycles a group): 69.7 us
+// with two, 71.7 with three at 16 sequences of 32768 tokens.
+constexpr int kPaWarpBytes = 2 * kPaK + kPaV;
 constexpr int kPaSmem = kPgWarps * kPaWarpBytes;
 constexpr int kPaTailTok = 16;                      // tokens of a tail item
 constexpr int kPaTailBytes = kPaTailTok * kPgRow;   // of K or V
@@ -58,8 +59,8 @@ static_assert(kPaSmem + 3072 <= 227 * 1024, "shared memory");
 // first group the sums are rarely scaled again.
 constexpr float kPaRoom = 5.f;
 constexpr float kPaLn2 = 0.6931471805599453f;
-// Where a running maximum starts: finite, so that a masked logit (-inf) minus
-// it is -inf and its weight 0.
+// Where a reference starts: finite, so that a masked logit (-inf) minus it is
+// -inf and its weight 0.
 constexpr float kPaMin = -1e30f;
 
 struct PagedAttendParams {
@@ -178,17 +179,17 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   __shared__ int pre[kMaxBatch + 1];
   __shared__ int wsum[kMaxBatch / 32];
   __shared__ int lens[kMaxBatch];
-  __shared__ uint64_t bars[kPgWarps][kPaKBuf + 1];
+  __shared__ uint64_t bars[kPgWarps][2 + 1];
   __shared__ int tail_seg[kPgWarps + 1], head_seg[kPgWarps + 1];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int hkv = p.c.num_kv_heads, G = p.G, H = p.c.num_heads;
   uint8_t* ring = pa_smem + warp * kPaWarpBytes;
   uint64_t* bar_k = bars[warp];
-  uint64_t* bar_v = &bars[warp][kPaKBuf];
+  uint64_t* bar_v = &bars[warp][2];
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i <= kPaKBuf; ++i) mbar_init(&bars[warp][i], 1);
+    for (int i = 0; i <= 2; ++i) mbar_init(&bars[warp][i], 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -271,14 +272,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
                                : static_cast<const uint8_t*>(p.c.pages) + kPaK) + d_off;
       const uint32_t bytes = tl ? kPaTailBytes : kPaV;
       mbar_expect_tx(bar_v, bytes);
-      bulk_g2s(ring + kPaKBuf * kPaK, src, bytes, bar_v, pol);
+      bulk_g2s(ring + 2 * kPaK, src, bytes, bar_v, pol);
     }
   };
 
   // ---- state of the current segment; lane (gid, tig): heads 2 tig, 2 tig + 1
   float acc[8][4];   // values, channels 16 mt + gid (+ 8), at the codes' scale 2^(pos - 24)
   float dz[4];       // rows 0-3: zero-point sums per channel group, row 4: mass
-  float m_run[2], kap[2];  // reference (running maximum - sh), kappa * 2^x of the query's scaling
+  float m_run[2], kap[2] = {0.f, 0.f};  // reference, kappa * 2^x of the query's scaling
   int sh = 15;             // e of the weights' reference
   uint32_t qf[16] = {};  // B fragment of the scaled query, head gid, times the codes' position factor
   int seg = 0;
@@ -286,20 +287,16 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   RowView rv = {};
   int my_head_seg = -1, my_tail_seg = -1;
 
-  auto reset_sums = [&]() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    dz[0] = dz[1] = dz[2] = dz[3] = 0.f;
-    m_run[0] = m_run[1] = kPaMin;
-    kap[0] = kap[1] = 0.f;
-    sh = 15;
-  };
   auto reset = [&](int s) {
     seg = s;
     int head;
     const int row = div_small(s, hkv, head);
     rv = row_of(row);
-    reset_sums();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    dz[0] = dz[1] = dz[2] = dz[3] = 0.f;
+    m_run[0] = m_run[1] = kPaMin;
+    sh = 15;
     const bool ok = gid < G;
     const uint16_t* qr = p.q + (int64_t)row * p.q_row + (size_t)(head * G + (ok ? gid : 0)) * kD;
     uint32_t w[16];
@@ -404,12 +401,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     }
   };
 
-  // Every warp's first keys are requested before any other copy, so that the
-  // first products start when a third of the buffers has been filled.  While
-  // they are on their way the loop's body runs once on nothing (a group with
-  // every token masked, whatever the buffers hold; reset() drops its sums):
-  // its instructions are fetched by then.
-  reset_sums();
+  // every warp's first keys are requested before any other copy, so that the
+  // first products start when a third of the buffers has been filled
   if (i0 < i1) {
     describe();
     __syncwarp();
@@ -418,14 +411,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   __syncthreads();
   if (i0 < i1) {
     issue_v(i0);
-    for (int x = 1; x < kPaKBuf; ++x)
-      if (i0 + x < i1) issue_k(i0 + x, x);
+    if (i0 + 1 < i1) issue_k(i0 + 1, 1);
   }
   int st = 0;
   uint32_t par_k = 0u, par_v = 0u;  // bit s: parity of key buffer s
-  bool failed = false;
+  bool failed = false, ready = false;  // ready: the next keys were seen to have come
   for (int i = i0; i < i1; ++i) {
-    if (i + kPaKBuf - base >= 32 && i + kPaKBuf < i1) {  // the next keys' descriptor is needed below
+    if (i + 2 - base >= 32 && i + 2 < i1) {  // the next keys' descriptor is needed below
       base = i;
       describe();
       __syncwarp();
@@ -442,10 +434,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     auto visible = [&](int t) {
       return !(kind & kItSkip) && t < rv.n && (t >= rv.win_lo || t < rv.sink_end);
     };
-    failed |= !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&bar_k[st], (par_k >> st) & 1u));
+    if (!ready) failed |= !mbar_wait_bounded(&bar_k[st], (par_k >> st) & 1u);
     par_k ^= 1u << st;
+    __syncwarp();
     const uint8_t* rk = ring + st * kPaK;
-    const uint8_t* rvb = ring + kPaKBuf * kPaK;
+    const uint8_t* rvb = ring + 2 * kPaK;
     if (!(kind & kItTail)) {
       // ---- logits (log2 units) u[mt][2 r + e]: token 16 mt + gid + 8 r, head
       // 2 tig + e.  Half of the code words at a time (slots 4 h .. 4 h + 3 in
@@ -504,7 +497,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         }
       }
       __syncwarp();
-      if (i + kPaKBuf < i1) issue_k(i + kPaKBuf, st);
+      if (i + 2 < i1) issue_k(i + 2, st);
+      const bool there = mbar_try_wait(bar_v, par_v);  // asked early, used below
       if (kind & kItMask) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
@@ -526,8 +520,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         pa[mt] = movmatrix_trans(pack_h2(approx_weight(u[mt][0], m_run[0]), approx_weight(u[mt][1], m_run[1])));
         pb[mt] = movmatrix_trans(pack_h2(approx_weight(u[mt][2], m_run[0]), approx_weight(u[mt][3], m_run[1])));
       }
-      failed |= !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_v, par_v));
+      if (!there) failed |= !mbar_wait_bounded(bar_v, par_v);
       par_v ^= 1u;
+      __syncwarp();
+      ready = i + 1 < i1 && mbar_try_wait(&bar_k[st ^ 1], (par_k >> (st ^ 1)) & 1u);
       {  // the group's largest value scale: 2^k <= s < 2^(k + 1) allows sh <= 15 - k
         const uint4 sw = *reinterpret_cast<const uint4*>(rvb + lane * 16);
         const uint32_t s2 = __vmaxu2(__vmaxu2(sw.x, sw.y), __vmaxu2(sw.z, sw.w));
@@ -609,7 +605,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         mma_bf16(d, a[0], a[1], a[2], a[3], qw[2 * ks], qw[2 * ks + 1]);
       }
       __syncwarp();
-      if (i + kPaKBuf < i1) issue_k(i + kPaKBuf, st);
+      if (i + 2 < i1) issue_k(i + 2, st);
+      const bool there = mbar_try_wait(bar_v, par_v);  // asked early, used below
       float u[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) u[x] = visible(t0 + gid + 8 * (x >> 1)) ? d[x] * p.kappa : -INFINITY;
@@ -623,8 +620,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         ph[x] = movmatrix_trans(hi);
         pl[x] = movmatrix_trans(pack_b2(w0 - bf_lo(hi), w1 - bf_hi(hi)));
       }
-      failed |= !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_v, par_v));
+      if (!there) failed |= !mbar_wait_bounded(bar_v, par_v);
       par_v ^= 1u;
+      __syncwarp();
+      ready = i + 1 < i1 && mbar_try_wait(&bar_k[st ^ 1], (par_k >> (st ^ 1)) & 1u);
       const uint32_t one = gid == 4 ? 0x3F803F80u : 0u;
       mma_bf16(dz, one, 0u, one, 0u, ph[0], ph[1]);
       mma_bf16(dz, one, 0u, one, 0u, pl[0], pl[1]);
@@ -643,7 +642,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       }
     }
     __syncwarp();
-    st = st + 1 == kPaKBuf ? 0 : st + 1;
+    st ^= 1;
     if (i + 1 < i1) issue_v(i + 1);
     if (kind & kItLast) {
       if (own_start) {
@@ -658,7 +657,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       store_partial(reinterpret_cast<float*>(ring));  // every copy has been used
     }
   }
-  if (failed && lane == 0) set_flag(p.flag, JFA_DEVERR_TIMEOUT);
+  if (failed) set_flag(p.flag, JFA_DEVERR_TIMEOUT);
   if (lane == 0) {
     tail_seg[warp] = my_tail_seg;
     head_seg[warp] = my_head_seg;
