@@ -57,10 +57,9 @@ __device__ __forceinline__ GroupParams group_params(float mn, float mx) {
 // Eight codes of a word: x[a][e][b] at bit 4 a + 16 e + 8 b, of the group [a][e].
 // t = 1.5 * 2^23 + round((x - z) / s): the sum of the shifted bit patterns less
 // that of 1.5 * 2^23's is the word.  The fp32 quotient's error is below 3e-6 at
-// 15; a word with one that near a border (or not a number) is formed again at
-// the end, by exact remainders.  bf16 numbers over an fp16 scale lie on a
-// border exactly about once in 900: each thread takes its own such words, one
-// in fourteen threads has one, so that a warp passes there once or twice.
+// 15; a word with one that near a border (or not a number) is formed again, by
+// exact remainders.  bf16 numbers over an fp16 scale lie on a border exactly
+// about once in 900, that is in every fourth warp's word.
 struct WordIn {
   float x[2][2][2], z[2][2], inv[2][2];
 };
@@ -70,7 +69,7 @@ __device__ __noinline__ uint32_t code_fp64(float x, float z, float s) {
 // The remainder d - (c + 1/2) s at the border next to the quotient is exact,
 // and so is its sign, where d = x - z is (both ways of undoing it agree); else
 // the fp64 quotient decides.
-__device__ __forceinline__ uint32_t word_exact(const WordIn& in) {
+__device__ __noinline__ uint32_t word_exact(WordIn in) {
   uint32_t word = 0u;
 #pragma unroll
   for (int a = 0; a < 2; ++a)
@@ -89,11 +88,11 @@ __device__ __forceinline__ uint32_t word_exact(const WordIn& in) {
     }
   return word;
 }
-__device__ __forceinline__ uint32_t quant_word(const WordIn& in, bool& near) {
+__device__ __forceinline__ uint32_t quant_word(const WordIn& in) {
   constexpr float kRound = 12582912.f;
   constexpr uint32_t kBits = 0x4B400000u;
   uint32_t word = 0u;
-  near = false;
+  bool near = false;
 #pragma unroll
   for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -104,7 +103,7 @@ __device__ __forceinline__ uint32_t quant_word(const WordIn& in, bool& near) {
         near |= !(fabsf(fmaf(d, in.inv[a][e], kRound - t)) <= 0.49999f);
         word += __float_as_uint(t) << (4 * a + 16 * e + 8 * b);
       }
-  return word - kBits * 0x11111111u;
+  return near ? word_exact(in) : word - kBits * 0x11111111u;
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -132,7 +131,7 @@ constexpr int kApThreads = 128;
 // Memory traffic is the bound for prompts (512 B of rows in and 152 B of
 // record out per token and KV head); a decode step's append (one row a
 // sequence) is bound by its launch and two dependent loads.
-__global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+__global__ void __launch_bounds__(kApThreads, 6) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   __shared__ int wsum[kApThreads / 32];
   __shared__ int mine[5];  // row, unit of it, first new row, their number, length
   __shared__ uint32_t rng[2][kApThreads / 32][kD / 2];  // key minima, maxima (channel pairs) by warp
@@ -214,12 +213,6 @@ __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_c
                                 : static_cast<const void*>(fresh + (int64_t)(tau - n0) * tok + 8 * ch);
       return *static_cast<const uint4*>(at);
     };
-    auto load_pair = [&](int t, int ch, int i) {  // its channels 2 i, 2 i + 1
-      const int tau = t0 + t;
-      const void* at = tau < n0 ? static_cast<const void*>(tail + tail_chunk(tau - nq0, ch) + 4 * i)
-                                : static_cast<const void*>(fresh + (int64_t)(tau - n0) * tok + 8 * ch + 2 * i);
-      return *static_cast<const uint32_t*>(at);
-    };
     bool bad = false;
     if (keys) {
       // lane (g4, w), pass k: tokens t = 16 mt + gid and t + 8 with 8 mt + gid = 16 k + 4 warp + g4
@@ -270,26 +263,6 @@ __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_c
         }
       }
       __syncthreads();
-      // a word's inputs: the channel pair's numbers of chunks w, w + 8 (c) and tokens t, t + 8 (r)
-      auto key_word = [&](const float4 par[2], uint32_t v00, uint32_t v01, uint32_t v10, uint32_t v11) {
-        const uint32_t v[2][2] = {{v00, v01}, {v10, v11}};
-        WordIn in;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          in.z[c][0] = par[c].x, in.inv[c][0] = par[c].y, in.z[c][1] = par[c].z, in.inv[c][1] = par[c].w;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            in.x[c][0][r] = bf_lo(v[c][r]);
-            in.x[c][1][r] = bf_hi(v[c][r]);
-          }
-        }
-        return in;
-      };
-      auto word_at = [&](int i, int k) {
-        const int q = q0 + 16 * k;
-        return reinterpret_cast<uint32_t*>(rec + off_kc() + (q >> 3) * 1024 + ((q & 7) * 4 + i) * 32 + 4 * w);
-      };
-      uint32_t again = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // channels 2 i, 2 i + 1 of the chunks: word w of lane 4 gid + i
         float4 par[2];
@@ -297,20 +270,22 @@ __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_c
         for (int c = 0; c < 2; ++c) par[c] = *reinterpret_cast<const float4*>(&zi[(w + 8 * c) * 10 + 2 * i]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          bool near;
-          const uint32_t word = quant_word(key_word(par, part(x[k][0][0], i), part(x[k][1][0], i), part(x[k][0][1], i),
-                                                    part(x[k][1][1], i)), near);
-          again |= (uint32_t)near << (2 * i + k);
-          if (page_ok) *word_at(i, k) = word;
-        }
-      }
-      for (; again && page_ok; again &= again - 1) {
-        const int i = (__ffs(again) - 1) >> 1, k = (__ffs(again) - 1) & 1, q = q0 + 16 * k, t = (q >> 3) * 16 + (q & 7);
-        float4 par[2];
+          WordIn in;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) par[c] = *reinterpret_cast<const float4*>(&zi[(w + 8 * c) * 10 + 2 * i]);
-        *word_at(i, k) = word_exact(key_word(par, load_pair(t, w, i), load_pair(t + 8, w, i), load_pair(t, w + 8, i),
-                                             load_pair(t + 8, w + 8, i)));
+          for (int c = 0; c < 2; ++c) {
+            in.z[c][0] = par[c].x, in.inv[c][0] = par[c].y, in.z[c][1] = par[c].z, in.inv[c][1] = par[c].w;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t v = part(x[k][r][c], i);
+              in.x[c][0][r] = bf_lo(v);
+              in.x[c][1][r] = bf_hi(v);
+            }
+          }
+          const uint32_t word = quant_word(in);
+          const int q = q0 + 16 * k;
+          if (page_ok)
+            *reinterpret_cast<uint32_t*>(rec + off_kc() + (q >> 3) * 1024 + ((q & 7) * 4 + i) * 32 + 4 * w) = word;
+        }
       }
     } else {
       // lane (hi8, m, tig): tokens t, t + 1 with t = 16 warp + 8 hi8 + 2 tig
@@ -359,8 +334,8 @@ __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_c
       }
       const int w8 = 2 * m + hi8;
       uint8_t* at = rec + off_vc(4) + (2 * warp + (w8 >> 2)) * 512 + tig * 16 + 4 * (w8 & 3);
-      // a word's inputs: the lower or upper channel of v [token][32-channel group][chunk]
-      auto value_word = [&](const uint32_t v[2][2][2], bool up) {
+#pragma unroll
+      for (int gid = 0; gid < 8; ++gid) {  // channel gid of the chunks
         WordIn in;
 #pragma unroll
         for (int hs = 0; hs < 2; ++hs)
@@ -369,35 +344,13 @@ __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const __grid_c
             in.z[hs][e] = z[e][hs];
             in.inv[hs][e] = inv[e][hs];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) in.x[hs][e][c] = up ? bf_hi(v[e][hs][c]) : bf_lo(v[e][hs][c]);
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t v = part(x[e][hs][c], gid >> 1);
+              in.x[hs][e][c] = gid & 1 ? bf_hi(v) : bf_lo(v);
+            }
           }
-        return in;
-      };
-      uint32_t again = 0u;
-#pragma unroll
-      for (int gid = 0; gid < 8; ++gid) {  // channel gid of the chunks
-        uint32_t v[2][2][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int hs = 0; hs < 2; ++hs)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) v[e][hs][c] = part(x[e][hs][c], gid >> 1);
-        bool near;
-        const uint32_t word = quant_word(value_word(v, gid & 1), near);
-        again |= (uint32_t)near << gid;
+        const uint32_t word = quant_word(in);
         if (page_ok) *reinterpret_cast<uint32_t*>(at + gid * 64) = word;
-      }
-      for (; again && page_ok; again &= again - 1) {
-        const int gid = __ffs(again) - 1;
-        uint32_t v[2][2][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int hs = 0; hs < 2; ++hs)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) v[e][hs][c] = load_pair(t + e, 2 * m + 8 * hs + c, gid >> 1);
-        *reinterpret_cast<uint32_t*>(at + gid * 64) = word_exact(value_word(v, gid & 1));
       }
     }
     if (bad) set_flag(p.flag, JFA_DEVERR_NONFINITE_QUANT);
