@@ -11,13 +11,15 @@ jfa_paged_* and jfa_qk_norm_rope calls.
     out = paged_decode_step(cache, q, k, v, table.seq_lens - 1, plan, ws)
 
 Unlike the calls on contiguous caches, these launch on torch's current stream
-when no stream is given, and on the device that holds the cache.
+when no stream is given, and on the device that holds the cache.  What a call
+allocates belongs to the stream it runs on.
 """
 from __future__ import annotations
 
 import ctypes
 import heapq
 import math
+import numbers
 
 import torch
 
@@ -69,7 +71,33 @@ def _rows(x, heads, dev, where, name):
     if x.dtype != _BF16 or len(shape) != 3 or shape[1] != heads or shape[2] != 128 or x.device != dev \
             or (strides[2] != 1 and x.numel()):
         _refuse(where, f"{name} must be bf16 [tokens, {heads}, {_lib.HEAD_DIM}] on {dev}, channels contiguous")
-    return x.data_ptr(), strides[0], strides[1]
+    # the stride of a dimension of one element means nothing
+    return x.data_ptr(), strides[0] if shape[0] > 1 else 0, strides[1] if heads > 1 else 0
+
+
+def _out_rows(x, like, heads, dev, where, name):
+    """_rows of an output: its input's shape, no two rows in one place."""
+    if x.shape != like.shape:
+        _refuse(where, f"{name} must have its input's shape")
+    at = _rows(x, heads, dev, where, name)
+    if (x.shape[0] > 1 and at[1] < 128) or (heads > 1 and at[2] < 128):
+        _refuse(where, f"{name} must not overlap itself")
+    return at
+
+
+def _fresh(make, stream, dev):
+    """make(), an output, from the memory of the call's stream."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _like(x, stream, dev):
+    """An output like x, contiguous."""
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _fresh(lambda: _like(x, None, dev), stream, dev)
 
 
 def _given(x, shape, dev, where, name):
@@ -179,19 +207,15 @@ def qk_norm_rope(q, k, positions, plan: RotaryPlan, q_weight=None, k_weight=None
     qw = None if q_weight is None else _weight(q_weight, dev, where, "q_weight")
     kw = None if k_weight is None else _weight(k_weight, dev, where, "k_weight")
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = _like(q, stream, dev)
         qop, qo_tok, qo_head = q_out.data_ptr(), h * 128, 128
-    elif q_out.shape != qs:
-        _refuse(where, "outputs must have their inputs' shapes")
     else:
-        qop, qo_tok, qo_head = _rows(q_out, h, dev, where, "q_out")
+        qop, qo_tok, qo_head = _out_rows(q_out, q, h, dev, where, "q_out")
     if k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        k_out = _like(k, stream, dev)
         kop, ko_tok, ko_head = k_out.data_ptr(), hkv * 128, 128
-    elif k_out.shape != ks:
-        _refuse(where, "outputs must have their inputs' shapes")
     else:
-        kop, ko_tok, ko_head = _rows(k_out, hkv, dev, where, "k_out")
+        kop, ko_tok, ko_head = _out_rows(k_out, k, hkv, dev, where, "k_out")
     r = Rope(t, h, hkv, plan.rotary_dim, plan.interleaved, wide, eps, plan.amplitude, qp, kp, qop, kop, q_tok,
              q_head, k_tok, k_head, qo_tok, qo_head, ko_tok, ko_head, qw, kw, positions.data_ptr(),
              plan.freq_ptr)
@@ -250,7 +274,8 @@ class PageTable:
         complete get pages; paged_append then brings the rows.  Returns the
         rows' ranges (int32 [batch + 1] on the device) for the second form.
         Without enough free pages or room in a row nothing changes."""
-        uniform = isinstance(n_new, int)
+        uniform = isinstance(n_new, numbers.Integral)
+        n_new = int(n_new) if uniform else n_new
         counts = [n_new if n else 0 for n in self.lens] if uniform else [int(n) for n in n_new]
         if len(counts) != self.batch or min(counts) < 0:
             _refuse("PageTable.grow", f"needs {self.batch} counts, none negative")
@@ -297,7 +322,7 @@ class PageTable:
     def fork(self, pairs):
         """Book (parent, child) forks; a child's earlier pages are released.
         Returns the pairs (int32 [n, 2] on the device) for paged_fork, which
-        every layer's cache then gets."""
+        every layer's cache gets before the table changes again."""
         pairs = [(int(a), int(b)) for a, b in pairs]
         children = [b for _, b in pairs]
         for a, b in pairs:
@@ -317,7 +342,8 @@ class PageTable:
     def compact(self):
         """Book the move of the pages in use to the front of the pool.  Returns
         (moves int32 [m, 2], remap int32 [n_pages]) on the device for
-        paged_move: every layer's cache gets the moves, one of them the remap."""
+        paged_move: every layer's cache gets the moves, one of them the remap,
+        before the table changes again."""
         used = [p for p in range(self.n_pages) if self._refs[p]]
         holes = [p for p in range(len(used)) if not self._refs[p]]
         goes = list(range(self.n_pages))
@@ -351,6 +377,7 @@ class PagedKVCache:
         s.table, s.seq_lens = table.table.data_ptr(), table.seq_lens.data_ptr()
 
         self._ref = ctypes.byref(s)
+        self.sizes = (table.batch, num_kv_heads)
 
     def struct(self) -> Paged:
         return self._struct
@@ -361,12 +388,14 @@ class PagedKVCache:
 
 
 class PagedWorkspace:
-    """Scratch of the paged calls on one cache, or on caches of the same sizes.
-    Calls that may run at the same time need one each."""
+    """Scratch of the paged calls on one cache, or on caches of as many
+    sequences and KV heads on its device.  Calls that may run at the same time
+    need one each."""
 
     def __init__(self, cache: PagedKVCache):
         self.buf = torch.zeros(cache.workspace_bytes, dtype=torch.uint8, device=cache.device)
-        self.ptr, self.nbytes, self.device = self.buf.data_ptr(), cache.workspace_bytes, self.buf.device
+        self.ptr, self.device = self.buf.data_ptr(), self.buf.device
+        self.sizes = (cache.table.batch, cache.num_kv_heads)
 
     def error_flag(self, cache: PagedKVCache, stream=None) -> int:
         with torch.cuda.device(cache.device):
@@ -380,8 +409,8 @@ class PagedWorkspace:
 
 
 def _ws(cache, ws, where):
-    if ws.nbytes < cache.workspace_bytes or ws.device != cache.device:
-        _refuse(where, f"workspace must hold {cache.workspace_bytes} bytes on {cache.device}")
+    if ws.sizes != cache.sizes or ws.device != cache.device:
+        _refuse(where, "workspace is of another number of sequences or KV heads, or on another device")
     return ws.ptr
 
 
@@ -411,11 +440,12 @@ def paged_gather(cache: PagedKVCache, cu, total: int, ws: PagedWorkspace, start=
     if total < 0:
         _refuse(where, "total must not be negative")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=_BF16, device=dev)
+        k_out = torch.empty(shape, dtype=_BF16, device=dev) if stream is None else \
+            _fresh(lambda: torch.empty(shape, dtype=_BF16, device=dev), stream, dev)
     else:
         _given(k_out, shape, dev, where, "k_out")
     if v_out is None:
-        v_out = torch.empty_like(k_out)
+        v_out = _like(k_out, stream, dev)
     else:
         _given(v_out, shape, dev, where, "v_out")
     cup = _int32(cu, batch + 1, dev, where, "cu")
@@ -436,10 +466,12 @@ def paged_attend(cache: PagedKVCache, q, ws: PagedWorkspace, scale=None, window:
     where = "paged_attend"
     dev, batch, heads = cache.device, cache.table.batch, cache.num_heads
     qp, q_row, q_head = _rows(q, heads, dev, where, "q")
+    if not (0 <= window < 2**31 and 0 <= sinks < 2**31):
+        _refuse(where, "window and sinks must be 0 or more, and below 2^31")
     if q.shape[0] != batch or (q_head != _lib.HEAD_DIM and heads > 1):
         _refuse(where, f"q must hold {batch} tokens, its heads contiguous")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _like(q, stream, dev)
     else:
         _given(out, q.shape, dev, where, "out")
     if lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != dev

@@ -590,7 +590,8 @@ typedef struct jfa_paged {
 } jfa_paged;            /* device pointers, 16-byte aligned (table, seq_lens: 4) */
 
 /* Workspace of the paged calls (256-byte aligned; zero before its first
- * call).  Calls that may run at the same time need one each. */
+ * call), for caches of one batch and num_kv_heads.  Calls that may run at the
+ * same time need one each. */
 int jfa_paged_workspace_bytes(const jfa_paged* cache, size_t* bytes);
 
 /* Append rows.  Row range [cu[b], cu[b + 1]) of k_new / v_new (bf16

@@ -767,6 +767,53 @@ def test_side_stream_and_two_graphs_on_one_workspace():
         assert torch.equal(out, w)
 
 
+def test_calls_on_a_given_stream():
+    """Stream objects and handles; outputs come from that stream's memory."""
+    lens = [300, 70]
+    table, cache, ws, rows = make(lens, 4, 2, seed=59)
+    q = rand_q(2, 4, 59).cuda()
+    want = jfa.paged_attend(cache, q, ws).clone()
+    cu = torch.tensor([0, 300, 370], dtype=torch.int32, device="cuda")
+    k, v = jfa.paged_gather(cache, cu, 370, ws)
+    plan = jfa.RotaryPlan(128)
+    pos = torch.arange(2, device="cuda")
+    turned = jfa.qk_norm_rope(q, k[:2], pos, plan)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        a = jfa.paged_attend(cache, q, ws, stream=stream)
+        b = jfa.paged_gather(cache, cu, 370, ws, stream=stream)
+        c = jfa.qk_norm_rope(q, k[:2], pos, plan, stream=stream)
+        side.synchronize()
+        assert torch.equal(a, want) and torch.equal(b[0], k) and torch.equal(b[1], v)
+        assert torch.equal(c[0], turned[0]) and torch.equal(c[1], turned[1])
+
+
+def test_one_sequence_of_odd_strides():
+    """The stride of a dimension of one element means nothing."""
+    table, cache, ws, rows = make([100], 1, 1, seed=61)
+    q = rand_q(1, 1, 61).cuda()
+    want = jfa.paged_attend(cache, q, ws).clone()
+    odd = q.as_strided((1, 1, D), (3, 5, 1))
+    assert torch.equal(jfa.paged_attend(cache, odd, ws), want)
+    table.grow(1)
+    jfa.paged_append(cache, odd, odd, ws)
+    kept = [(torch.cat((rows[0][0], q.cpu())), torch.cat((rows[0][1], q.cpu())))]
+    torch.cuda.synchronize()
+    assert ws.error_flag(cache) == 0
+    check_cache(table, cache, kept)
+
+
+def test_output_in_the_query_s_place():
+    lens = [3000, 0, 64]
+    table, cache, ws, rows = make(lens, 8, 2, seed=63)
+    q = rand_q(3, 8, 63).cuda()
+    want = jfa.paged_attend(cache, q, ws).clone()
+    got = jfa.paged_attend(cache, q, ws, out=q)
+    torch.cuda.synchronize()
+    assert got is q and torch.equal(q, want)
+
+
 def test_two_workspaces_at_the_same_time():
     lens = [9000, 64, 3000]
     table, cache, ws, rows = make(lens, 8, 2, seed=57)

@@ -68,6 +68,15 @@ def test_grow_refuses_without_changing_anything():
         _check_book(t)
 
 
+def test_grow_takes_whole_numbers_of_any_kind():
+    import numpy as np
+    t = jfa.PageTable(2, 4, 4, device="cpu")
+    t.grow(np.array([3, 0]))
+    t.grow(np.int64(2))
+    assert t.lens == [5, 0]
+    _check_book(t)
+
+
 def test_fork_shares_and_free_counts():
     t = jfa.PageTable(4, 10, 4, device="cpu")
     t.grow([200, 70, 0, 0])
@@ -186,7 +195,8 @@ def _paged(**kw):
 def test_workspace_bytes():
     n = _lib.jfa_paged_workspace_bytes(_paged())
     part = 8 * 132 * 4                               # a partial of 8 heads
-    assert n == 256 + 256 + 192 * (2 + 16) * part
+    # flag, tickets, two partials of each block and one of each of its 12 warps
+    assert n == 256 + 256 + 192 * (2 + 12) * part
     assert _lib.jfa_paged_workspace_bytes(_paged(batch=256, num_kv_heads=8)) == n + 256 * 8 * 4 - 256
 
 
@@ -284,6 +294,8 @@ def test_python_layer_refusals():
     rows = torch.zeros(2, 2, 128, dtype=torch.bfloat16)
     q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
     cu = torch.zeros(3, dtype=torch.int32)
+    # a workspace of fewer KV heads, and one of more
+    other = jfa.PagedWorkspace(jfa.PagedKVCache(t, 8, 4))
     plan = jfa.RotaryPlan(device="cpu")
     refused = [
         lambda: jfa.paged_append(cache, rows.float(), rows, ws),
@@ -299,6 +311,12 @@ def test_python_layer_refusals():
         lambda: jfa.paged_attend(cache, q[:, :4], ws),
         lambda: jfa.paged_attend(cache, q.transpose(0, 1).contiguous().transpose(0, 1), ws),
         lambda: jfa.paged_attend(cache, q, ws, scale=-1.0),
+        lambda: jfa.paged_attend(cache, q, ws, window=-1),
+        lambda: jfa.paged_attend(cache, q, ws, window=2**32 + 5),
+        lambda: jfa.paged_attend(cache, q, ws, window=5, sinks=2**31),
+        lambda: jfa.paged_attend(cache, q, other),
+        lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, q_out=q[:1].expand(2, 8, 128)),
+        lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, k_out=rows[:, :1].expand(2, 2, 128)),
         lambda: jfa.paged_attend(cache, q, ws, scale=math.inf),
         lambda: jfa.paged_attend(cache, q, ws, out=q.float()),
         lambda: jfa.paged_attend(cache, q, ws, lse=torch.zeros(2, 4)),
