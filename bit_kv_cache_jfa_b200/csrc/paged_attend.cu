@@ -124,6 +124,12 @@ struct Cut {
   }
 };
 
+// The segment at one end of a CTA's range, where other CTAs share it.
+struct RangeEnd {
+  int seg, sa, items, ca, cb;  // its first item and their number, its CTAs ca .. cb
+  bool shared, last;           // last: this CTA's items were the last to come
+};
+
 enum : int { kItTail = 1, kItMask = 2, kItSkip = 4, kItFirst = 8, kItLast = 16 };
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -150,6 +156,12 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 2^x, the hardware's: 2^-22 relative; what is below 2^-126 becomes 0
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 // a b - c
 __device__ __forceinline__ uint32_t h2_rest(uint32_t a, uint32_t b, uint32_t c) {
@@ -181,7 +193,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   __shared__ int lens[kMaxBatch];
   __shared__ uint64_t bars[kPgWarps][2 + 1];
   __shared__ int tail_seg[kPgWarps + 1], head_seg[kPgWarps + 1];
-  __shared__ int s_last;
+  __shared__ RangeEnd ends[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int hkv = p.c.num_kv_heads, G = p.G, H = p.c.num_heads;
   uint8_t* ring = pa_smem + warp * kPaWarpBytes;
@@ -412,6 +424,15 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   if (i0 < i1) {
     issue_v(i0);
     if (i0 + 1 < i1) issue_k(i0 + 1, 1);
+  }
+  if (warp < 2) {  // while the first copies are on their way
+    const int x = warp == 0 ? r0 : r1 - 1, row = batch_find(pre, x), items = row_of(row).items;
+    int rel;
+    const int head = div_small(x - pre[row], items, rel), sa = x - rel;
+    // finished here, or one segment fills the range
+    const bool alone = (sa >= r0 && sa + items <= r1) || (warp == 1 && sa <= r0);
+    const RangeEnd e = {row * hkv + head, sa, items, ctas.part_of(sa), ctas.part_of(sa + items - 1), !alone, false};
+    if (lane == 0) ends[warp] = e;
   }
   int st = 0;
   uint32_t par_k = 0u, par_v = 0u;  // bit s: parity of key buffer s
@@ -722,7 +743,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
       M = fmaxf(__shfl_sync(0xFFFFFFFFu, M, 0), mg);
-      const float fl = mine ? exp2f(ml - M) : 0.f, fg = wh >= 0 ? exp2f(mg - M) : 0.f;
+      const float fl = mine ? exp2_ftz(ml - M) : 0.f, fg = wh >= 0 ? exp2_ftz(mg - M) : 0.f;
       float L = mine ? fl * pl[1] : 0.f;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
@@ -753,31 +774,22 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
 
   // ---- the segments at the range's ends that other CTAs share
   __syncthreads();
+  if (warp < 2 && lane == 0 && ends[warp].shared) {
+    const RangeEnd e = ends[warp];
+    const uint32_t mine = (uint32_t)(min(e.sa + e.items, r1) - max(e.sa, r0));
+    __threadfence();  // the block's partials (before the barrier) come before its ticket
+    if (atomicAdd(&p.ticket[e.seg], mine) + mine == (uint32_t)e.items) {
+      __threadfence();  // the others' partials are read after it
+      p.ticket[e.seg] = 0u;
+      ends[warp].last = true;
+    }
+  }
+  __syncthreads();
 #pragma unroll 1
   for (int end = 0; end < 2; ++end) {
-    const int x = end == 0 ? r0 : r1 - 1;
-    const int row = batch_find(pre, x), items = row_of(row).items;
-    int rel;
-    const int head = div_small(x - pre[row], items, rel), s = row * hkv + head;
-    const int sa = x - rel, sb = sa + items;
-    if (sa >= r0 && sb <= r1) continue;      // finished here
-    if (end == 1 && sa <= r0) continue;      // one segment fills the range
-    if (tid == 0) {
-      const uint32_t mine = (uint32_t)(min(sb, r1) - max(sa, r0));
-      __threadfence();  // the block's partials (before the barrier) come before its ticket
-      const bool all = atomicAdd(&p.ticket[s], mine) + mine == (uint32_t)(sb - sa);
-      if (all) {
-        __threadfence();  // the others' partials are read after it
-        p.ticket[s] = 0u;
-      }
-      s_last = all;
-    }
-    const int ca = ctas.part_of(sa), cb = ctas.part_of(sb - 1);
-    __syncthreads();
-    const bool last = s_last != 0;
-    __syncthreads();
-    if (!last) continue;
-    // G heads, 16 / G warps each on every so-manieth CTA's partial
+    if (!ends[end].last) continue;
+    const int s = ends[end].seg, sa = ends[end].sa, ca = ends[end].ca, cb = ends[end].cb;
+    // G heads, 12 / G warps each on every so-manieth CTA's partial
     const int per = kPgWarps / G, h = warp % G, sub = warp / G;
     auto part = [&](int c) {
       return p.part_cta + ((size_t)c * 2 + (sa < ctas.begin(c) ? 0 : 1)) * kPgPart + h * kPartStride;
@@ -800,7 +812,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         float n = M;
 #pragma unroll
         for (int i = 0; i < kAt; ++i) n = fmaxf(n, ml[i].x);
-        const float fo = exp2f(M - n);
+        const float fo = exp2_ftz(M - n);
         M = n;
         L *= fo;
         O.x *= fo;
@@ -809,7 +821,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         O.w *= fo;
 #pragma unroll
         for (int i = 0; i < kAt; ++i) {
-          const float f = exp2f(ml[i].x - M);
+          const float f = exp2_ftz(ml[i].x - M);
           L = fmaf(ml[i].y, f, L);
           O.x = fmaf(v[i].x, f, O.x);
           O.y = fmaf(v[i].y, f, O.y);
@@ -831,7 +843,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int i = 0; i < per; ++i) {
         const float* src = reinterpret_cast<const float*>(pa_smem) + (h + i * G) * kPartStride;
-        const float f = exp2f(src[0] - M);
+        const float f = exp2_ftz(src[0] - M);
         const float4 v = *reinterpret_cast<const float4*>(src + 4 + 4 * lane);
         L = fmaf(src[1], f, L);
         O.x = fmaf(v.x, f, O.x);
