@@ -51,9 +51,10 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 //   kRpInter: chunks l and l + 8, pairs within them;
 //   kRpHalfOdd: chunks l and l + 8; the partners come through shared memory
 //     (fp32, a 9-float pitch a chunk against bank conflicts).
-// HBM-bound when there are many tokens: 512 B a head.  A token's sines are
-// formed again by each of its warps (about 100 of a unit's 300 instructions):
-// that costs less than the wait of a whole block for one token's.
+// HBM-bound when there are many tokens: 512 B a head; 8192 tokens of 32 and 8
+// heads take 30.1 us, 5.6 TB/s, 64 tokens 2.6 us.  A token's sines are formed
+// again by each of its warps (446 instructions a warp in all): a block per
+// token, which forms them once and waits for them, took 95.8 us.
 template <int MODE>
 __global__ void __launch_bounds__(32 * kRpWarps) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 cs_s[kRpWarps][kD / 2];
