@@ -45,8 +45,11 @@ def _run(where, dev, stream, *args):
     """Call the library's ``where`` on dev and ``stream``.  These calls take
     microseconds on the device: what the host adds is kept small (one look at
     the current device and stream, no context manager when dev is current)."""
-    fn, st = getattr(_lib.load(), where), _handle(dev, stream)
-    if torch.cuda.current_device() == dev.index:
+    fn = _calls.get(where)
+    if fn is None:
+        fn = _calls[where] = getattr(_lib.load(), where)
+    st = _handle(dev, stream)
+    if _current_device() == dev.index:
         status = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -55,6 +58,9 @@ def _run(where, dev, stream, *args):
         check(status, where)
 
 
+_calls = {}
+# The current device without the check that CUDA is up (every tensor here is on one).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # The handle of a device's current stream without a Stream object (2 us) around it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -440,8 +446,8 @@ def paged_gather(cache: PagedKVCache, cu, total: int, ws: PagedWorkspace, start=
     if total < 0:
         _refuse(where, "total must not be negative")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=_BF16, device=dev) if stream is None else \
-            _fresh(lambda: torch.empty(shape, dtype=_BF16, device=dev), stream, dev)
+        k_out = cache.tail_k.new_empty(shape) if stream is None else \
+            _fresh(lambda: cache.tail_k.new_empty(shape), stream, dev)
     else:
         _given(k_out, shape, dev, where, "k_out")
     if v_out is None:
