@@ -47,9 +47,8 @@ constexpr int kPaK = 512 + 4096;   // key scales, zero points and codes
 constexpr int kPaV = 1024 + 4096;  // the same of the values
 // Per warp two key buffers and one value buffer: while the values of a group
 // are used the next keys have arrived, and while keys are used the values
-// arrive.  A third key buffer gains nothing (a warp does not wait for copies
-// once the first have come, about 130 of its 4500 cycles a group): 69.7 us
-// with two, 71.7 with three at 16 sequences of 32768 tokens.
+// arrive.  A third key buffer makes it 3 % slower: a warp does not wait for
+// copies once the first have come (130 of its 4500 cycles a group).
 constexpr int kPaWarpBytes = 2 * kPaK + kPaV;
 constexpr int kPaSmem = kPgWarps * kPaWarpBytes;
 constexpr int kPaTailTok = 16;                      // tokens of a tail item
@@ -73,7 +72,7 @@ struct PagedAttendParams {
   uint16_t* out;
   float* lse;
   float* part_cta;   // [grid][2][8][132]
-  float* part_warp;  // [grid][16][8][132]
+  float* part_warp;  // [grid][kPgWarps][8][132]
   uint32_t* ticket;  // [batch][H_kv]
   uint32_t* flag;
   int64_t q_row;
