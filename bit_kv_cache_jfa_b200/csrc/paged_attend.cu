@@ -53,10 +53,15 @@ constexpr int kPaWarpBytes = 2 * kPaK + kPaV;
 constexpr int kPaSmem = kPgWarps * kPaWarpBytes;
 constexpr int kPaTailTok = 16;                      // tokens of a tail item
 constexpr int kPaTailBytes = kPaTailTok * kPgRow;   // of K or V
-constexpr int kPaMinItems = 8;                      // items per CTA, at least
+// Items per CTA, at least: few CTAs leave warps alone on their scheduler, many
+// leave more partials to merge over CTAs (2.5 us where there is one).  Between
+// 4 and 12 neither end wins: one sequence of 300 tokens, 2 KV heads, 8.7 (4)
+// and 7.4 us (8); 8 of 2000, 4 KV heads, 13.0, 11.2 and 14.1 (4, 8, 12); one of
+// 2000, 8 KV heads, 10.0, 10.5 and 11.3; 32 of 200, 8.4, 9.7 and 13.9.
+constexpr int kPaMinItems = 8;
 static_assert(kPaTailBytes <= kPaK && kPaTailBytes <= kPaV, "a tail item fits the buffers");
 static_assert(kPgPart * 4 <= kPaWarpBytes, "a warp's partial fits its buffers");
-static_assert(kPaSmem + 3072 <= 227 * 1024, "shared memory");
+static_assert(kPaSmem + 4096 <= 227 * 1024, "shared memory");
 // Room that a raised reference leaves under the largest weight that fits: a
 // maximum that grows by less than 2^5 raises nothing, so that after a warp's
 // first group the sums are rarely scaled again.

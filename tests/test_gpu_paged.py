@@ -538,6 +538,40 @@ def test_empty_page_calls():
     assert k.shape == (0, 1, D) and ws.error_flag(cache) == 0
 
 
+def test_pages_past_32_bit_offsets():
+    """A pool of 4.7 GB whose last pages are in use: append, read-back,
+    attention, move."""
+    hkv, n = 8, 400
+    table = jfa.PageTable(2, 60000, 16)
+    cache = jfa.PagedKVCache(table, 8, hkv)
+    assert cache.pages.numel() > 2**32
+    ws = jfa.PagedWorkspace(cache)
+    k, v = make_rows(2 * n, hkv, 67)
+    rows = [(k[:n], v[:n]), (k[n:], v[n:])]
+    pages = list(range(59988, 60000))
+    table.grow([n, n])
+    table.rows = [pages[:6], pages[6:]]
+    table._refs = [0] * 60000
+    for p in pages:
+        table._refs[p] = 1
+    table.table[:, :6] = torch.tensor(table.rows, dtype=torch.int32)
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    jfa.paged_append(cache, k.cuda(), v.cuda(), ws, cu)
+    check_cache(table, cache, rows)
+    q = rand_q(2, 8, 67)
+    check_attend(cache, ws, rows, q, rms=RMS)
+    got = jfa.paged_gather(cache, cu, 2 * n, ws)
+    want = np.concatenate([Ref(*r).k.transpose(1, 0, 2) for r in rows])
+    err = np.abs(got[0].cpu().double().numpy() - want)
+    assert (err <= (BF16 + 2.0**-23) * np.abs(want) + 2.0**-133).all()
+    moves, remap = table.compact()
+    jfa.paged_move(cache, moves, ws, remap)
+    torch.cuda.synchronize()
+    assert ws.error_flag(cache) == 0 and sorted(table.rows[0] + table.rows[1]) == list(range(12))
+    check_cache(table, cache, rows)
+    check_attend(cache, ws, rows, q, rms=RMS)
+
+
 # ---------------------------------------------------------------------------
 # what the kernels themselves refuse
 # ---------------------------------------------------------------------------
@@ -738,6 +772,24 @@ def test_prompts_then_decode_steps(graph):
             jfa.paged_move(cache, moves, ws, remap)
     assert ws.error_flag(cache) == 0
     check_cache(table, cache, kept)
+
+
+def test_decode_step_with_idle_rows():
+    lens = [64, 0, 70, 0]
+    table, cache, ws, rows = make(lens, 4, 2, seed=73)
+    plan = jfa.RotaryPlan(64)
+    table.grow(1)
+    new = torch.randn(4, 8, D, generator=gen(73)).bfloat16().cuda()
+    pos = table.seq_lens - 1
+    out = jfa.paged_decode_step(cache, new[:, :4], new[:, 4:6], new[:, 6:], pos, plan, ws)
+    q, k = jfa.qk_norm_rope(new[:, :4], new[:, 4:6], pos, plan)
+    torch.cuda.synchronize()
+    assert ws.error_flag(cache) == 0
+    kept = [(torch.cat((a, k[b:b + 1].cpu())), torch.cat((c, new[b:b + 1, 6:].cpu()))) if lens[b] else (a, c)
+            for b, (a, c) in enumerate(rows)]
+    check_cache(table, cache, kept)
+    assert torch.equal(out, check_attend(cache, ws, kept, q.cpu()))
+    assert (out[1] == 0).all() and (out[3] == 0).all()
 
 
 def test_side_stream_and_two_graphs_on_one_workspace():
