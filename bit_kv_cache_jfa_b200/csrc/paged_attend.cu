@@ -444,6 +444,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   }
   int st = 0;
   uint32_t par_k = 0u, par_v = 0u;  // bit s: parity of key buffer s
+  // rows of the mass and zero-point product: lanes gid < 4 the zero points, 4 ones
+  const uint32_t z_mask = gid < 4 ? 0xFFFFFFFFu : 0u, z_one = gid == 4 ? kOneH2 : 0u;
   bool failed = false, ready = false;  // ready: the next keys were seen to have come
   for (int i = i0; i < i1; ++i) {
     if (i + 2 - base >= 32 && i + 2 < i1) {  // the next keys' descriptor is needed below
@@ -553,6 +555,20 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       par_v ^= 1u;
       __syncwarp();
       ready = i + 1 < i1 && mbar_try_wait(&bar_k[st ^ 1], (par_k >> (st ^ 1)) & 1u);
+      if (kind & kItMask) {
+        // What a masked token holds does not matter, infinities too: its scales
+        // and zero points become 0 where they lie (lane l: tokens 2 l, 2 l + 1),
+        // so that the products below need no branch.
+        const uint32_t m = half_mask(visible(t0 + 2 * lane), visible(t0 + 2 * lane + 1));
+        uint32_t* at = reinterpret_cast<uint32_t*>(ring + 2 * kPaK + vs_scale_off(2 * lane, 0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          at[2 * j] &= m;
+          at[128 + 2 * j] &= m;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into the buffer
+        __syncwarp();
+      }
       {  // the group's largest value scale: 2^k <= s < 2^(k + 1) allows sh <= 15 - k
         const uint4 sw = *reinterpret_cast<const uint4*>(rvb + lane * 16);
         const uint32_t s2 = __vmaxu2(__vmaxu2(sw.x, sw.y), __vmaxu2(sw.z, sw.w));
@@ -574,24 +590,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       for (int kk = 0; kk < 4; ++kk) {
         const uint4 s0 = *reinterpret_cast<const uint4*>(rvb + kk * 128 + tig * 32);
         const uint4 s1 = *reinterpret_cast<const uint4*>(rvb + kk * 128 + tig * 32 + 16);
-        uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-        uint32_t za0 = gid == 4 ? kOneH2 : 0u, za2 = za0;
-        if (gid < 4) {
-          const uint2 zz = *reinterpret_cast<const uint2*>(rvb + 512 + kk * 128 + tig * 32 + gid * 8);
-          za0 = zz.x;
-          za2 = zz.y;
-        }
-        if (kind & kItMask) {  // what a masked token holds does not matter, infinities too
-          const int t = t0 + 16 * kk + 2 * tig;
-          const uint32_t ma = half_mask(visible(t), visible(t + 1)), mb = half_mask(visible(t + 8), visible(t + 9));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sv[2 * j] &= ma;
-            sv[2 * j + 1] &= mb;
-          }
-          za0 &= ma;
-          za2 &= mb;
-        }
+        const uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        const uint2 zz = *reinterpret_cast<const uint2*>(rvb + 512 + kk * 128 + tig * 32 + (gid & 3) * 8);
+        const uint32_t za0 = (zz.x & z_mask) | z_one, za2 = (zz.y & z_mask) | z_one;
         uint32_t bh[4][2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
