@@ -301,7 +301,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   float dz[4];       // rows 0-3: zero-point sums per channel group, row 4: mass
   float m_run[2], kap[2] = {0.f, 0.f};  // reference, kappa * 2^x of the query's scaling
   int sh = 15;             // e of the weights' reference
-  uint32_t qf[16] = {};  // B fragment of the scaled query, head gid, times the codes' position factor
+  // B fragment of the scaled query, head gid, times the codes' position factor;
+  // of each four pairs the second and third change places
+  uint32_t qf[16] = {};
   int seg = 0;
   bool own_start = false;  // the segment's first item was this warp's
   RowView rv = {};
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
 #pragma unroll
     for (int pp = 0; pp < 16; ++pp) {
       const float f = pp < 8 ? 16.f * down : down;  // KeyPos<4>::factor
-      qf[pp] = pack_h2(bf_lo(w[pp]) * f, bf_hi(w[pp]) * f);
+      qf[(pp & 12) | (pp & 1) << 1 | (pp >> 1 & 1)] = pack_h2(bf_lo(w[pp]) * f, bf_hi(w[pp]) * f);
     }
     kap[0] = p.kappa * __shfl_sync(0xFFFFFFFFu, up, 8 * tig);
     kap[1] = p.kappa * __shfl_sync(0xFFFFFFFFu, up, 8 * tig + 4);
@@ -477,7 +479,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       // these slots, the bias (the remainders' share and the zero points), and
       // four chains of MMAs, one an m-tile.
       float u[4][4] = {};
-      float bz[2][4] = {}, cr[4] = {};  // bz[0]: slots 0-7, with the factor 16
+      // [0]: slots 0-7, with the factor 16.  A lane's zero points of four pairs,
+      // as they lie, are an A operand of two k-steps at once: rows gid have the
+      // first and third pair, rows gid + 8 the second and fourth, so the upper
+      // rows of one product (bz) and the lower of the other (by) count.
+      float bz[2][4] = {}, by[2][4] = {}, cr[4] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t qb[2][4];
@@ -486,19 +492,20 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
           const int i4 = h + 2 * n;
           const uint4 sv = *reinterpret_cast<const uint4*>(rk + i4 * 64 + tig * 16);
           const uint4 zv = *reinterpret_cast<const uint4*>(rk + (4 + i4) * 64 + tig * 16);
-          const uint32_t sk[4] = {sv.x, sv.y, sv.z, sv.w}, zk[4] = {zv.x, zv.y, zv.z, zv.w};
+          const uint32_t sk[4] = {sv.x, sv.y, sv.z, sv.w};
+          const uint32_t* q1 = qf + 4 * i4;
           const uint32_t c15 = n == 0 ? 0x000F000Fu : 0x00F000F0u;  // twice 7.5, at the codes' bit position
           uint32_t lo[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            qb[n][x] = h2_mul(qf[4 * i4 + x], sk[x]);
-            lo[x] = h2_rest(qf[4 * i4 + x], sk[x], qb[n][x]);
+            const int y = (x & 1) << 1 | x >> 1;
+            qb[n][x] = h2_mul(q1[y], sk[x]);
+            lo[x] = h2_rest(q1[y], sk[x], qb[n][x]);
           }
-#pragma unroll
-          for (int x = 0; x < 4; x += 2) {
-            mma16816(bz[n], zk[x], zk[x], zk[x + 1], zk[x + 1], qf[4 * i4 + x], qf[4 * i4 + x + 1]);
-            mma16816(cr, c15, c15, c15, c15, lo[x], lo[x + 1]);
-          }
+          mma16816(bz[n], zv.x, zv.y, zv.z, zv.w, q1[0], q1[1]);
+          mma16816(cr, c15, c15, c15, c15, lo[0], lo[1]);
+          mma16816(by[n], zv.x, zv.y, zv.z, zv.w, q1[2], q1[3]);
+          mma16816(cr, c15, c15, c15, c15, lo[2], lo[3]);
         }
         uint32_t w[4][4];
 #pragma unroll
@@ -519,7 +526,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float bk = (fmaf(cr[e], 0.5f * KeyPos<4>::unscale, bz[1][e]) + bz[0][e] * 0.0625f) * kap[e];
+        const float bk = (fmaf(cr[e], 0.5f * KeyPos<4>::unscale, bz[1][e] + by[1][2 + e]) +
+                          (bz[0][e] + by[0][2 + e]) * 0.0625f) * kap[e];
         const float ku = kap[e] * KeyPos<4>::unscale;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
