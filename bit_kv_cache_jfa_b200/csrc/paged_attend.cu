@@ -10,10 +10,10 @@
 // What bounds it: the cache is read once, 152 B per packed token and KV head,
 // for 4 * 128 * G flop, far under the tensor rate: HBM, if the SM keeps up
 // with unpacking 4-bit codes.  It keeps up to about 85 % of HBM's rate while it
-// streams (940 instructions a record, 450 of them on the half-rate logic
+// streams (917 instructions a record, 475 of them on the half-rate logic
 // pipe); the start and the merges add 10 us: 16 sequences of 32768 tokens, 4 KV
-// heads of 8 query heads, 61.7 us (floor 46.7), one of 131072 tokens, 8 KV
-// heads, 37.3 us (24.3).  So the codes never leave the registers of the
+// heads of 8 query heads, 59.9 us (floor 46.7), one of 131072 tokens, 8 KV
+// heads, 36.7 us (24.3).  So the codes never leave the registers of the
 // warp that loads them: they are stored in the order of the mma.sync
 // fragments, one AND turns a 32-bit word into a ready fp16 operand (subnormal
 // code * 2^(pos - 24), exact), and the scales go to the other operand:

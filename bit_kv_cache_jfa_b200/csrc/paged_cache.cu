@@ -133,8 +133,8 @@ constexpr int kApThreads = 128;
 // table -> rows what holds it at 19 us for 7600 rows of 8 KV heads (floor 6.6
 // us): 1600 instructions a warp, 590 of them for codes on borders.  Keys and
 // values in one block of 256 threads with the rows staged in shared memory
-// take a quarter longer (cold 31 us against 25).  A decode step's append (one row a sequence) is bound by its
-// launch and two dependent loads.
+// take a quarter longer (cold 31 us against 25).  A decode step's append (one
+// row a sequence) is bound by its launch and two dependent loads.
 __global__ void __launch_bounds__(kApThreads, 6) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   __shared__ int wsum[kApThreads / 32];
   __shared__ int mine[5];  // row, unit of it, first new row, their number, length
@@ -683,7 +683,7 @@ static_assert(kPgRec == 152 * 4 * 16, "record in four chunks a thread");
 // CTAs [0, n * H_kv): one record each, all its loads before its stores (no
 // page is both source and destination).  CTAs after them: a table row each.
 // HBM-bound: 2 * 9728 B per page and KV head; 1000 pages of 8 KV heads with
-// the fork before them take 27.4 us, 93 % of the copy rate.
+// the fork before them take 27.3 us, 94 % of the copy rate.
 __global__ void __launch_bounds__(kMvThreads) paged_move_kernel(const __grid_constant__ PagedMoveParams p) {
   const int tid = threadIdx.x, hkv = p.c.num_kv_heads;
   pdl_wait();

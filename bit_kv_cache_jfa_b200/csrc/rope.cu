@@ -52,7 +52,7 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 //   kRpHalfOdd: chunks l and l + 8; the partners come through shared memory
 //     (fp32, a 9-float pitch a chunk against bank conflicts).
 // HBM-bound when there are many tokens: 512 B a head; 8192 tokens of 32 and 8
-// heads take 30.1 us, 5.6 TB/s, 64 tokens 2.6 us.  A token's sines are formed
+// heads take 30.0 us, 5.6 TB/s, 64 tokens 2.6 us.  A token's sines are formed
 // again by each of its warps (446 instructions a warp in all): a block per
 // token, which forms them once and waits for them, took 95.8 us.
 template <int MODE>
