@@ -62,6 +62,9 @@ constexpr int kPaMinItems = 8;
 static_assert(kPaTailBytes <= kPaK && kPaTailBytes <= kPaV, "a tail item fits the buffers");
 static_assert(kPgPart * 4 <= kPaWarpBytes, "a warp's partial fits its buffers");
 static_assert(kPaSmem + 4096 <= 227 * 1024, "shared memory");
+// Where a CTA's share is below this many items, its ends move to the ends of
+// segments of at most kPgWarps items.
+constexpr int kPaSnap = 64;
 // Room that a raised reference leaves under the largest weight that fits: a
 // maximum that grows by less than 2^5 raises nothing, so that after a warp's
 // first group the sums are rarely scaled again.
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   __shared__ int pre[kMaxBatch + 1];
   __shared__ int wsum[kMaxBatch / 32];
   __shared__ int lens[kMaxBatch];
+  __shared__ __align__(16) int has_short[kPgWarps];  // a segment of at most kPgWarps items, by warp
   __shared__ uint64_t bars[kPgWarps][2 + 1];
   __shared__ int tail_seg[kPgWarps + 1], head_seg[kPgWarps + 1];
   __shared__ RangeEnd ends[2];
@@ -220,6 +224,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       items = row_view(n, p.window, p.sinks).items * hkv;
       lens[tid] = n;
     }
+    const bool any = __any_sync(0xFFFFFFFFu, items > 0 && items <= kPgWarps * hkv);
+    if (lane == 0) has_short[warp] = any;
     batch_prefix(items, pre, wsum);
   }
   auto row_of = [&](int row) { return row_view(lens[row], p.window, p.sinks); };
@@ -235,7 +241,24 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   const int C = min((int)gridDim.x, (T + kPaMinItems - 1) / kPaMinItems);
   if ((int)blockIdx.x >= C) return;
   const Cut ctas(T, C);
-  const int r0 = ctas.begin(blockIdx.x), r1 = ctas.begin(blockIdx.x + 1);
+  int r0 = ctas.begin(blockIdx.x), r1 = ctas.begin(blockIdx.x + 1);
+  static_assert(kPgWarps == 12 && kMaxBatch <= 8 * 32, "has_short in two loads");
+  const int4 h0 = *reinterpret_cast<const int4*>(has_short), h1 = *reinterpret_cast<const int4*>(has_short + 4);
+  if (T < kPaSnap * C && (h0.x | h0.y | h0.z | h0.w | h1.x | h1.y | h1.z | h1.w)) {
+    // A cut inside a short segment moves to the segment's nearer end: nothing
+    // to merge over CTAs there.  Lane 0 looks up r0, lane 1 r1.
+    const int x = lane == 0 ? r0 : r1;
+    int to = x;
+    if (lane < 2 && x < T) {
+      const int row = batch_find(pre, x), items = row_of(row).items;
+      int rel;
+      div_small(x - pre[row], items, rel);
+      if (items <= kPgWarps) to = x - rel + (2 * rel >= items ? items : 0);
+    }
+    r0 = __shfl_sync(0xFFFFFFFFu, to, 0);
+    r1 = __shfl_sync(0xFFFFFFFFu, to, 1);
+    if (r0 == r1) return;
+  }
   const int nw = min(kPgWarps, r1 - r0);  // the first nw warps have items
   const Cut warps(r1 - r0, nw);
   const int i0 = warp < nw ? r0 + warps.begin(warp) : r1, i1 = warp < nw ? r0 + warps.begin(warp + 1) : r1;
