@@ -54,17 +54,21 @@ constexpr int kPaSmem = kPgWarps * kPaWarpBytes;
 constexpr int kPaTailTok = 16;                      // tokens of a tail item
 constexpr int kPaTailBytes = kPaTailTok * kPgRow;   // of K or V
 // Items per CTA, at least: few CTAs leave warps alone on their scheduler, many
-// leave more partials to merge over CTAs (2.5 us where there is one).  Between
-// 4 and 12 neither end wins: one sequence of 300 tokens, 2 KV heads, 8.7 (4)
-// and 7.4 us (8); 8 of 2000, 4 KV heads, 13.0, 11.2 and 14.1 (4, 8, 12); one of
-// 2000, 8 KV heads, 10.0, 10.5 and 11.3; 32 of 200, 8.4, 9.7 and 13.9.
-constexpr int kPaMinItems = 8;
+// leave more partials to merge over CTAs (2.5 us where there is one).  4 against
+// 8: one sequence of 1000 / 4000 tokens, 8 KV heads, 9.9 / 10.2 and 11.2 / 10.5
+// us; 32 of 200, 8.5 and 10.0; 17 of 171..1203 under a window of 270, 8.9 and
+// 10.6; 8 of 2000, 4 KV heads, where shares of 8 meet the segments' ends, 12.9
+// and 11.0.  2 is slower again: 11.6 against 10.2 for 2 of 3000.
+constexpr int kPaMinItems = 4;
+// Where a CTA's share is below this many items, its ends move to the ends of
+// segments of at most kPgWarps items (one a warp): 96 sequences of 57..312
+// tokens, 8 KV heads, 18.9 -> 14.9 us, 3 of 273..502 10.7 -> 8.8.  Larger shares
+// would not feel the merge.  Segments of up to 18: mixed (12.9 -> 11.8 for 96
+// under a window, 9.9 -> 11.1 for one of 1000).
+constexpr int kPaSnap = 64;
 static_assert(kPaTailBytes <= kPaK && kPaTailBytes <= kPaV, "a tail item fits the buffers");
 static_assert(kPgPart * 4 <= kPaWarpBytes, "a warp's partial fits its buffers");
 static_assert(kPaSmem + 4096 <= 227 * 1024, "shared memory");
-// Where a CTA's share is below this many items, its ends move to the ends of
-// segments of at most kPgWarps items.
-constexpr int kPaSnap = 64;
 // Room that a raised reference leaves under the largest weight that fits: a
 // maximum that grows by less than 2^5 raises nothing, so that after a warp's
 // first group the sums are rarely scaled again.
