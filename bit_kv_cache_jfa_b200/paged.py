@@ -86,8 +86,12 @@ def _out_rows(x, like, heads, dev, where, name):
     if x.shape != like.shape:
         _refuse(where, f"{name} must have its input's shape")
     at = _rows(x, heads, dev, where, name)
-    if (x.shape[0] > 1 and at[1] < 128) or (heads > 1 and at[2] < 128):
-        _refuse(where, f"{name} must not overlap itself")
+    room = 128  # of a row, then of the rows along the smaller stride
+    for stride, count in sorted(((at[1], x.shape[0]), (at[2], heads))):
+        if count > 1:
+            if stride < room:
+                _refuse(where, f"{name} must not overlap itself")
+            room = stride * count
     return at
 
 

@@ -317,6 +317,8 @@ def test_python_layer_refusals():
         lambda: jfa.paged_attend(cache, q, other),
         lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, q_out=q[:1].expand(2, 8, 128)),
         lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, k_out=rows[:, :1].expand(2, 2, 128)),
+        lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, q_out=q.as_strided((2, 8, 128), (256, 128, 1))),
+        lambda: jfa.qk_norm_rope(q, rows, cu[:2], plan, q_out=q.as_strided((2, 8, 128), (128, 128, 1))),
         lambda: jfa.paged_attend(cache, q, ws, scale=math.inf),
         lambda: jfa.paged_attend(cache, q, ws, out=q.float()),
         lambda: jfa.paged_attend(cache, q, ws, lse=torch.zeros(2, 4)),
