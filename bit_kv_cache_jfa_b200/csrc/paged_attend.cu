@@ -18,16 +18,19 @@
 // fragments, one AND turns a 32-bit word into a ready fp16 operand (subnormal
 // code * 2^(pos - 24), exact), and the scales go to the other operand:
 //   logits  A = key codes (16 tokens x 16 channels),
-//           B = fp16(q_c s_c) of the KV head's <= 8 query heads;
+//           B = q_c s_c of the KV head's <= 8 query heads, hi = fp16(q_c s_c)
+//           and lo = q_c s_c - hi, one product each;
 //   values  A = value codes (16 channels x 16 tokens), B = fp16(p_t s_tj).
 //
-// Rounding q_c s_c to fp16 errs by d_c, |d_c| <= 2^-11 |q_c s_c|.  A code is
-// 7.5 + (k' - 7.5), so the part of the error that all 64 tokens share is
-// 7.5 sum_c d_c: it is computed (one chain of 8 MMAs on the remainders) and
-// added.  What is left, sum_c d_c (k'_c - 7.5), is of the size that rounding
-// p_t to fp16 has as well: about 3e-4 of a weight at unit-normal data with
-// outlier channels, against 2^-9 of the bf16 output.  A second fp16 limb of
-// q s would double the key MMAs of a group (32 of 84).
+// q_c s_c has 19 bits (8 of bf16, 11 of fp16), so hi + lo is it exactly (but
+// for what falls under fp16's smallest step, 2^-25 of 8 max |q|): a logit is
+// as exact as its 32-bit sums, whatever the range of the keys.  With hi alone
+// its error grows with that range (0.07 where a channel is a hundred times
+// the others' size and the query four times), for 6 % of the time less: 60.0
+// against 64.2 us, 16 sequences of 32768 tokens, 4 KV heads of 8 query heads.
+// The weights are fp16, and so is a weight times its value's scale: 2^-11 at
+// most each, 3e-4 of an output at unit-normal data against the 1.6e-3 of its
+// bf16, and no more at any other; further halves would double the value MMAs.
 // The query is scaled by a power of two to [1/8, 1/4) first, so that q s,
 // times the 16 of the codes' position, stays in fp16's range at every scale a
 // record can hold (131008 / 15).  The weights are taken against a reference
@@ -502,18 +505,18 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     if (!(kind & kItTail)) {
       // ---- logits (log2 units) u[mt][2 r + e]: token 16 mt + gid + 8 r, head
       // 2 tig + e.  Half of the code words at a time (slots 4 h .. 4 h + 3 in
-      // their low, 8 more in their high nibbles): the B operand fp16(q s F) of
-      // these slots, the bias (the remainders' share and the zero points), and
-      // four chains of MMAs, one an m-tile.
+      // their low, 8 more in their high nibbles): the B operands of these slots,
+      // hi = fp16(q s F) and lo = q s F - hi, the zero points' share, and four
+      // chains of MMAs, one an m-tile.
       float u[4][4] = {};
       // [0]: slots 0-7, with the factor 16.  A lane's zero points of four pairs,
       // as they lie, are an A operand of two k-steps at once: rows gid have the
       // first and third pair, rows gid + 8 the second and fourth, so the upper
       // rows of one product (bz) and the lower of the other (by) count.
-      float bz[2][4] = {}, by[2][4] = {}, cr[4] = {};
+      float bz[2][4] = {}, by[2][4] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t qb[2][4];
+        uint32_t hi[2][4], lo[2][4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {  // slots 4 h + 8 n ..
           const int i4 = h + 2 * n;
@@ -521,18 +524,14 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
           const uint4 zv = *reinterpret_cast<const uint4*>(rk + (4 + i4) * 64 + tig * 16);
           const uint32_t sk[4] = {sv.x, sv.y, sv.z, sv.w};
           const uint32_t* q1 = qf + 4 * i4;
-          const uint32_t c15 = n == 0 ? 0x000F000Fu : 0x00F000F0u;  // twice 7.5, at the codes' bit position
-          uint32_t lo[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int y = (x & 1) << 1 | x >> 1;
-            qb[n][x] = h2_mul(q1[y], sk[x]);
-            lo[x] = h2_rest(q1[y], sk[x], qb[n][x]);
+            hi[n][x] = h2_mul(q1[y], sk[x]);
+            lo[n][x] = h2_rest(q1[y], sk[x], hi[n][x]);
           }
           mma16816(bz[n], zv.x, zv.y, zv.z, zv.w, q1[0], q1[1]);
-          mma16816(cr, c15, c15, c15, c15, lo[0], lo[1]);
           mma16816(by[n], zv.x, zv.y, zv.z, zv.w, q1[2], q1[3]);
-          mma16816(cr, c15, c15, c15, c15, lo[2], lo[3]);
         }
         uint32_t w[4][4];
 #pragma unroll
@@ -545,16 +544,21 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const uint32_t mask = 0x000F000Fu << (4 * n);
+            uint32_t a[4][4];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              a[mt][0] = w[mt][x] & mask, a[mt][1] = (w[mt][x] >> 8) & mask;
+              a[mt][2] = w[mt][x + 1] & mask, a[mt][3] = (w[mt][x + 1] >> 8) & mask;
+              mma16816(u[mt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], hi[n][x], hi[n][x + 1]);
+            }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
-              mma16816(u[mt], w[mt][x] & mask, (w[mt][x] >> 8) & mask, w[mt][x + 1] & mask,
-                       (w[mt][x + 1] >> 8) & mask, qb[n][x], qb[n][x + 1]);
+              mma16816(u[mt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], lo[n][x], lo[n][x + 1]);
           }
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float bk = (fmaf(cr[e], 0.5f * KeyPos<4>::unscale, bz[1][e] + by[1][2 + e]) +
-                          (bz[0][e] + by[0][2 + e]) * 0.0625f) * kap[e];
+        const float bk = (bz[1][e] + by[1][2 + e] + (bz[0][e] + by[0][2 + e]) * 0.0625f) * kap[e];
         const float ku = kap[e] * KeyPos<4>::unscale;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {

@@ -1,0 +1,107 @@
+"""GPU: how exact the attention over the paged 4-bit cache is, whatever the
+ranges of keys and values: bounds in which logits are of 32 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_kv_cache_jfa_b200 as jfa
+from test_gpu_paged import BF16, D, Ref, gen, make_rows
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(ref, q, scale):
+    """(out, lse, bound, lse_bound) of queries [H][128] over ref's cache, in 64
+    bits.
+
+    A logit is a sum of products that are exact in 32 bits (the query times a
+    key's scale is held in two halves, 2^-25 of 8 max|q| lost under fp16's
+    smallest step, times a code of at most 15), of codes and zero points apart:
+    about 20 additions, cut to 32 bits each, are 20 * 2^-23 < 2^-18 of the terms'
+    size, scaling and the rest 2^-20 of the logit.
+    A weight is rounded to fp16, and once more times its value's scale (2^-11
+    each at most).  The largest lies in [2^10, 2^15], so that 2^-25 and less is
+    lost of it at fp16's bottom, 2^-35 of the largest."""
+    hkv, h = ref.k.shape[0], q.shape[0]
+    out, bound, lse, lse_bound = np.zeros((h, D)), np.zeros((h, D)), np.zeros(h), np.zeros(h)
+    c, nq = ref.c, ref.nq
+    for i in range(h):
+        j = i // (h // hkv)
+        k, v, a = ref.k[j], ref.v[j], np.abs(q[i])
+        x = scale * (k @ q[i])
+        m = x.max()
+        p = np.exp(x - m)
+        lse[i] = m + np.log(p.sum())
+        p /= p.sum()
+        out[i] = p @ v
+        size, ce = np.abs(k) @ a, np.abs(v).copy()
+        lost = np.zeros((len(p), D))
+        if nq:
+            s = np.repeat(c.k_scale[0, j].astype(float), 64, 0)
+            z = np.repeat(np.abs(c.k_zero[0, j].astype(float)), 64, 0)
+            size[:nq] += (s * c.k_codes[0, j] + z) @ a
+            vs = np.repeat(c.v_scale[0, j].astype(float), 32, -1)
+            vz = np.repeat(np.abs(c.v_zero[0, j].astype(float)), 32, -1)
+            ce[:nq] = vs * c.v_codes[0, j] + vz
+            lost[:nq] = 15 * vs + vz
+        e = scale * (2.0**-18 * size + 2.0**-22 * 15 * 128 * a.max()) + 2.0**-20 * (1 + np.abs(x))
+        w = 2.0**-11
+        bound[i] = p @ ((np.expm1(e) + 2 * w + 2.0**-16)[:, None] * (ce + np.abs(out[i]))) \
+            + 2.0**-35 * p.max() * (lost + np.abs(out[i])).sum(0) + (BF16 + 2.0**-16) * np.abs(out[i])
+        lse_bound[i] = -np.log1p(-min(p @ (np.expm1(e) + w) + 2.0**-35 * p.max() * len(p), 0.9)) \
+            + 2.0**-20 * (1 + abs(lse[i]))
+    return out, lse, bound, lse_bound
+
+
+# Relative error over all outputs, root mean square: bf16's rounding, at most
+# 2^-8 and uniform, 2^-8 / sqrt(3) = 2.26e-3; the weights' two, 2^-11 / sqrt(3)
+# each, of codes times scales, which are about three times the values'
+# size: 8.5e-4 and 2.8e-4; a logit's 32 bits 2e-4.  Together 2.45e-3.
+RMS = 2.5e-3
+
+
+def check(lens, k, v, q, rms=RMS, scale=1 / math.sqrt(D)):
+    heads, hkv = q.shape[1], k.shape[1]
+    n_pages = sum(n // 64 + 1 for n in lens)
+    table = jfa.PageTable(len(lens), n_pages, max(lens) // 64 + 1)
+    cache = jfa.PagedKVCache(table, heads, hkv)
+    ws = jfa.PagedWorkspace(cache)
+    jfa.paged_append(cache, k.cuda(), v.cuda(), ws, table.grow(lens))
+    lse = torch.zeros(len(lens), heads, device="cuda")
+    out = jfa.paged_attend(cache, q.cuda(), ws, scale=scale, lse=lse)
+    torch.cuda.synchronize()
+    assert ws.error_flag(cache) == 0
+    got, lse, at, want = out.cpu().double().numpy(), lse.cpu().double().numpy(), 0, []
+    for b, n in enumerate(lens):
+        o, l, bound, l_bound = reference(Ref(k[at:at + n], v[at:at + n]), q[b].double().numpy(), scale)
+        at += n
+        want.append(o)
+        assert (np.abs(lse[b] - l) <= l_bound).all(), (b, np.abs(lse[b] - l) / l_bound)
+        assert (np.abs(got[b] - o) <= bound).all(), (b, (np.abs(got[b] - o) / bound).max())
+    want = np.stack(want)
+    assert np.linalg.norm(got - want) <= rms * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("big,q_scale", [(1.0, 1.0), (10.0, 1.0), (30.0, 1.0), (100.0, 1.0), (100.0, 4.0),
+                                         (1000.0, 0.5)])
+@pytest.mark.parametrize("heads,hkv", [(8, 1), (6, 2), (1, 1)])
+def test_keys_of_any_range(big, q_scale, heads, hkv):
+    """A few key channels far larger than the others: what their products are
+    rounded to must not grow with them."""
+    lens = [257, 4000, 641, 1]
+    k, v = make_rows(sum(lens), hkv, int(big) + heads, outliers=0)
+    wide = torch.ones(D)
+    wide[torch.randperm(D, generator=gen(int(big)))[:4]] = big
+    q = (torch.randn(len(lens), heads, D, generator=gen(heads)) * q_scale).bfloat16()
+    check(lens, (k.float() * wide).bfloat16(), v, q)
+
+
+def test_wide_keys_of_a_long_sequence():
+    lens = [32768]
+    k, v = make_rows(lens[0], 1, 77, outliers=0)
+    wide = torch.ones(D)
+    wide[[3, 40, 77, 120]] = 30.0
+    q = torch.randn(1, 8, D, generator=gen(78)).bfloat16()
+    check(lens, (k.float() * wide).bfloat16(), v, q)
