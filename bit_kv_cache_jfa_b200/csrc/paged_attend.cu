@@ -34,12 +34,15 @@
 // The query is scaled by a power of two to [1/8, 1/4) first, so that q s,
 // times the 16 of the codes' position, stays in fp16's range at every scale a
 // record can hold (131008 / 15).  The weights are taken against a reference
-// r, p_t = 2^(u - r), set so that the largest is at most 2^e: e is 15 where
-// the value scales are below 2 and falls (for the rest of the segment) where a
-// larger one would take p_t s_tj past fp16.  r rises only when a weight would
-// pass 2^e, and then to leave it at 2^(e - 5): sums are rarely scaled again,
-// and weights down to 2^-24 of the largest keep their 11 bits, however many
-// tokens share the mass.
+// r, p_t = 2^(u - r), that rises only when one would pass 2^15, and then to
+// leave it at 2^10: sums are rarely scaled again, and the largest weight lies
+// between 2^10 and 2^15.  So a weight keeps its 11 bits down to 2^-24 of the
+// largest at least, and loses less than 2^-35 of it below: the mass and the
+// zero points' sums hold however many tokens share the mass.  The codes' sums
+// are scaled by a power of two 2^x, by which the largest value scale of a group
+// comes into [2^-3, 2): where x > 0 it goes to the scales (exactly), else to
+// the weights of that group (past fp16 otherwise), so that small values lose
+// no more, and large ones cost the groups beside them nothing.
 #include "jfa_approx.cuh"
 #include "jfa_paged.cuh"
 
@@ -72,10 +75,15 @@ constexpr int kPaSnap = 64;
 static_assert(kPaTailBytes <= kPaK && kPaTailBytes <= kPaV, "a tail item fits the buffers");
 static_assert(kPgPart * 4 <= kPaWarpBytes, "a warp's partial fits its buffers");
 static_assert(kPaSmem + 4096 <= 227 * 1024, "shared memory");
-// Room that a raised reference leaves under the largest weight that fits: a
-// maximum that grows by less than 2^5 raises nothing, so that after a warp's
-// first group the sums are rarely scaled again.
+// The largest weight is 2^kPaTop at most (fp16 ends at 2^16); the room that a
+// raised reference leaves under that: a maximum that grows by less than 2^5
+// raises nothing, so that after a warp's first group the sums are rarely
+// scaled again.
+constexpr float kPaTop = 15.f;
 constexpr float kPaRoom = 5.f;
+// Bits by which a group's value scales may be smaller than those that the
+// codes' sums are scaled for before that changes.
+constexpr int kPaSlack = 3;
 constexpr float kPaLn2 = 0.6931471805599453f;
 // Where a reference starts: finite, so that a masked logit (-inf) minus it is
 // -inf and its weight 0.
@@ -327,10 +335,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
   };
 
   // ---- state of the current segment; lane (gid, tig): heads 2 tig, 2 tig + 1
-  float acc[8][4];   // values, channels 16 mt + gid (+ 8), at the codes' scale 2^(pos - 24)
+  float acc[8][4];   // codes' part, channels 16 mt + gid (+ 8), times 2^(pos - 24) and 2^vx
   float dz[4];       // rows 0-3: zero-point sums per channel group, row 4: mass
   float m_run[2], kap[2] = {0.f, 0.f};  // reference, kappa * 2^x of the query's scaling
-  int sh = 15;             // e of the weights' reference
+  int vx = 0;              // the values' codes are summed times 2^vx
   // B fragment of the scaled query, head gid, times the codes' position factor;
   // of each four pairs the second and third change places
   uint32_t qf[16] = {};
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     dz[0] = dz[1] = dz[2] = dz[3] = 0.f;
     m_run[0] = m_run[1] = kPaMin;
-    sh = 15;
+    vx = 0;
     const bool ok = gid < G;
     const uint16_t* qr = p.q + (int64_t)row * p.q_row + (size_t)(head * G + (ok ? gid : 0)) * kD;
     uint32_t w[16];
@@ -374,6 +382,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     kap[1] = p.kappa * __shfl_sync(0xFFFFFFFFu, up, 8 * tig + 4);
   };
 
+  auto pow2 = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
+
   // the segment's sums out of the registers: dst[h * stride + ...] = m, l, acc
   auto store_partial = [&](float* dst) {
 #pragma unroll
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         float* row = dst + h * kPartStride;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-          const float us = (mt >> 2) ? 1048576.0f : 16777216.0f;
+          const float us = pow2(((mt >> 2) ? 20 : 24) - vx);
           row[4 + 16 * mt + gid] = fmaf(acc[mt][e], us, zj[mt >> 1]);
           row[4 + 16 * mt + gid + 8] = fmaf(acc[mt][2 + e], us, zj[mt >> 1]);
         }
@@ -413,7 +423,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + ((size_t)row * H + head * G + h) * kD;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-          const float us = (mt >> 2) ? 1048576.0f : 16777216.0f;
+          const float us = pow2(((mt >> 2) ? 20 : 24) - vx);
           o[16 * mt + gid] = __float2bfloat16_rn(fmaf(acc[mt][e], us, zj[mt >> 1]) * inv);
           o[16 * mt + gid + 8] = __float2bfloat16_rn(fmaf(acc[mt][2 + e], us, zj[mt >> 1]) * inv);
         }
@@ -438,18 +448,17 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     dz[2] *= a0;
     dz[3] *= a1;
   };
-  // the lane's largest logits of heads 2 tig + e: where one is more than 2^sh
-  // over its reference, the references go to kPaRoom below 2^sh over the largest
+  // the lane's largest logits of heads 2 tig + e: where one is more than kPaTop
+  // over its reference, the references go to kPaRoom below kPaTop over the largest
   auto raise_max = [&](float mx0, float mx1) {
-    const float top = (float)sh;
-    if (__any_sync(0xFFFFFFFFu, mx0 > m_run[0] + top || mx1 > m_run[1] + top)) {
+    if (__any_sync(0xFFFFFFFFu, mx0 > m_run[0] + kPaTop || mx1 > m_run[1] + kPaTop)) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, o));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, o));
       }
-      rescale(mx0 > m_run[0] + top ? mx0 - (top - kPaRoom) : m_run[0],
-              mx1 > m_run[1] + top ? mx1 - (top - kPaRoom) : m_run[1]);
+      rescale(mx0 > m_run[0] + kPaTop ? mx0 - (kPaTop - kPaRoom) : m_run[0],
+              mx1 > m_run[1] + kPaTop ? mx1 - (kPaTop - kPaRoom) : m_run[1]);
     }
   };
 
@@ -608,23 +617,23 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into the buffer
         __syncwarp();
       }
-      {  // the group's largest value scale: 2^k <= s < 2^(k + 1) allows sh <= 15 - k
+      {  // the group's largest value scale, times 2^fit, is in [1, 2)
         const uint4 sw = *reinterpret_cast<const uint4*>(rvb + lane * 16);
         const uint32_t s2 = __vmaxu2(__vmaxu2(sw.x, sw.y), __vmaxu2(sw.z, sw.w));
         const uint32_t smax = __reduce_max_sync(0xFFFFFFFFu, max(s2 & 0xFFFFu, s2 >> 16));
-        const int fit = max(30 - (int)(smax >> 10), 0);
-        if (fit < sh) {
-          const float d = (float)(sh - fit);
-          sh = fit;
-          rescale(m_run[0] + d, m_run[1] + d);
-          const uint32_t down = pack_h2(exp2f(-d), exp2f(-d));
+        const int fit = max(15 - (int)(smax >> 10), -14);  // (at -14 the scale is infinite or NaN)
+        if (vx > fit || (vx < fit - kPaSlack && smax != 0u)) {
+          const float f = pow2(fit - vx);
+          vx = fit;
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            pa[mt] = h2_mul(pa[mt], down);
-            pb[mt] = h2_mul(pb[mt], down);
-          }
+          for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[mt][x] *= f;
         }
       }
+      // 2^vx as fp16x2, to the scales or to the weights.  Branches around the 40
+      // multiplications save 1 % at unit-normal values and cost as much at others.
+      const uint32_t s_up = (uint32_t)(15 + max(vx, 0)) * 0x04000400u, p_down = (uint32_t)(15 + min(vx, 0)) * 0x04000400u;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const uint4 s0 = *reinterpret_cast<const uint4*>(rvb + kk * 128 + tig * 32);
@@ -632,11 +641,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         const uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
         const uint2 zz = *reinterpret_cast<const uint2*>(rvb + 512 + kk * 128 + tig * 32 + (gid & 3) * 8);
         const uint32_t za0 = (zz.x & z_mask) | z_one, za2 = (zz.y & z_mask) | z_one;
+        const uint32_t va = h2_mul(pa[kk], p_down), vb = h2_mul(pb[kk], p_down);
         uint32_t bh[4][2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          bh[j][0] = h2_mul(pa[kk], sv[2 * j]);
-          bh[j][1] = h2_mul(pb[kk], sv[2 * j + 1]);
+          bh[j][0] = h2_mul(va, h2_mul(sv[2 * j], s_up));
+          bh[j][1] = h2_mul(vb, h2_mul(sv[2 * j + 1], s_up));
         }
         mma16816(dz, za0, 0u, za2, 0u, pa[kk], pb[kk]);
         const uint4 v0 = *reinterpret_cast<const uint4*>(rvb + 1024 + (2 * kk) * 512 + lane * 16);
@@ -705,7 +715,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         float o[4] = {0.f, 0.f, 0.f, 0.f};
         mma_bf16(o, a[0] & ma, a[1] & ma, a[2] & mb, a[3] & mb, ph[0], ph[1]);
         mma_bf16(o, a[0] & ma, a[1] & ma, a[2] & mb, a[3] & mb, pl[0], pl[1]);
-        const float ps = (mt >> 2) ? 0x1p-20f : 0x1p-24f;  // to the accumulator's scale
+        const float ps = pow2(vx - ((mt >> 2) ? 20 : 24));  // to the accumulator's scale
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[mt][x] = fmaf(o[x], ps, acc[mt][x]);
       }

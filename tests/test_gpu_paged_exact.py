@@ -22,8 +22,10 @@ def reference(ref, q, scale):
     about 20 additions, cut to 32 bits each, are 20 * 2^-23 < 2^-18 of the terms'
     size, scaling and the rest 2^-20 of the logit.
     A weight is rounded to fp16, and once more times its value's scale (2^-11
-    each at most).  The largest lies in [2^10, 2^15], so that 2^-25 and less is
-    lost of it at fp16's bottom, 2^-35 of the largest."""
+    each at most).  The largest lies in [2^10, 2^15], so that what is lost at
+    fp16's bottom, 2^-25, is 2^-35 of the largest; of a weight times a scale
+    (which counts for a code of 15 at most), that times 8 of the largest scale
+    of the 64 tokens, and times 8 of it again where it is 2 or more."""
     hkv, h = ref.k.shape[0], q.shape[0]
     out, bound, lse, lse_bound = np.zeros((h, D)), np.zeros((h, D)), np.zeros(h), np.zeros(h)
     c, nq = ref.c, ref.nq
@@ -45,7 +47,8 @@ def reference(ref, q, scale):
             vs = np.repeat(c.v_scale[0, j].astype(float), 32, -1)
             vz = np.repeat(np.abs(c.v_zero[0, j].astype(float)), 32, -1)
             ce[:nq] = vs * c.v_codes[0, j] + vz
-            lost[:nq] = 15 * vs + vz
+            top = c.v_scale[0, j].astype(float).reshape(-1, 64 * 4).max(1).repeat(64)[:, None]
+            lost[:nq] = 15 * 8 * top * np.maximum(8 * top, 1) + vz
         e = scale * (2.0**-18 * size + 2.0**-22 * 15 * 128 * a.max()) + 2.0**-20 * (1 + np.abs(x))
         w = 2.0**-11
         bound[i] = p @ ((np.expm1(e) + 2 * w + 2.0**-16)[:, None] * (ce + np.abs(out[i]))) \
@@ -105,3 +108,35 @@ def test_wide_keys_of_a_long_sequence():
     wide[[3, 40, 77, 120]] = 30.0
     q = torch.randn(1, 8, D, generator=gen(78)).bfloat16()
     check(lens, (k.float() * wide).bfloat16(), v, q)
+
+
+@pytest.mark.parametrize("size,loud", [(1.0, False), (1.0, True), (2.0**-9, False), (2.0**-14, False)])
+def test_mass_spread_over_many_tokens_far_below_one(size, loud):
+    """One token of value 0 above 20000 of a weight of 2^-24 each, which alone
+    make the output: with values of about 1, with values thousands of times as
+    large among them (which no weight reaches), with small values.  256
+    sequences share the pages, so that a warp goes over most of one."""
+    n, batch, hkv = 20001, 256, 8
+    k, v = make_rows(n, hkv, 91, outliers=0)
+    k *= 0.02
+    k[n // 2] = 16.6 * math.sqrt(D) / D
+    v = ((v.float() * 0.5 + 3) * size).bfloat16()
+    v[n // 2] = 0
+    if loud:
+        for g in range(0, n // 64, 8):
+            k[64 * g:64 * g + 64] = -3.0
+            v[64 * g:64 * g + 64] *= 2048
+    q = torch.ones(1, hkv, D).bfloat16()
+    table = jfa.PageTable(batch, 320, 320)
+    cache = jfa.PagedKVCache(table, hkv, hkv)
+    ws = jfa.PagedWorkspace(cache)
+    jfa.paged_append(cache, k.cuda(), v.cuda(), ws, table.grow([n] + [0] * (batch - 1)))
+    jfa.paged_fork(cache, table.fork([(0, b) for b in range(1, batch)]), ws)
+    lse = torch.zeros(batch, hkv, device="cuda")
+    got = jfa.paged_attend(cache, q.cuda().expand(batch, hkv, D), ws, lse=lse).cpu().double().numpy()
+    assert ws.error_flag(cache) == 0
+    out, l, bound, l_bound = reference(Ref(k, v), q[0].double().numpy(), 1 / math.sqrt(D))
+    for b in range(batch):
+        assert np.linalg.norm(got[b] - out) <= RMS * np.linalg.norm(out), b
+        assert (np.abs(got[b] - out) <= bound).all(), b
+        assert (np.abs(lse[b].cpu().double().numpy() - l) <= l_bound).all(), b
