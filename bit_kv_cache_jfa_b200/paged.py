@@ -20,6 +20,7 @@ import ctypes
 import heapq
 import math
 import numbers
+import operator
 
 import torch
 
@@ -429,7 +430,12 @@ def paged_append(cache: PagedKVCache, k, v, ws: PagedWorkspace, cu=None, stream=
     strides that are multiples of 8).  cu (int32 [batch + 1], device): rows
     cu[b] .. cu[b + 1] - 1 are sequence b's newest tokens; without it every
     sequence has T / batch, and idle ones (length 0) are left alone.  The
-    table's lengths already count the new tokens (PageTable.grow)."""
+    table's lengths already count the new tokens (PageTable.grow).
+
+    Once for each growth: a group that completes is packed from what the tail
+    held, and the tail is overwritten.  A second append at the same lengths (a
+    warm-up before a capture, a call repeated) would pack the new rows in place
+    of the old ones."""
     where = "paged_append"
     dev, batch = cache.device, cache.table.batch
     ka, va = _rows(k, cache.num_kv_heads, dev, where, "k"), _rows(v, cache.num_kv_heads, dev, where, "v")
@@ -474,23 +480,42 @@ def paged_attend(cache: PagedKVCache, q, ws: PagedWorkspace, scale=None, window:
     of 8).  Returns out bf16 [B, H, 128], zeros for an idle sequence; lse (fp32
     [B, H], if given) gets the natural logarithm of the softmax's sum."""
     where = "paged_attend"
+    args = _attend_args(cache, q, out, lse, scale, window, sinks, where)
+    return _attend(cache, q, ws, *args, where, stream)
+
+
+def _attend_args(cache, q, out, lse, scale, window, sinks, where):
+    """Checks of paged_attend's arguments but for q's memory: (out, lse, scale, window, sinks)."""
     dev, batch, heads = cache.device, cache.table.batch, cache.num_heads
-    qp, q_row, q_head = _rows(q, heads, dev, where, "q")
+    window, sinks = operator.index(window), operator.index(sinks)
     if not (0 <= window < 2**31 and 0 <= sinks < 2**31):
         _refuse(where, "window and sinks must be 0 or more, and below 2^31")
-    if q.shape[0] != batch or (q_head != _lib.HEAD_DIM and heads > 1):
-        _refuse(where, f"q must hold {batch} tokens, its heads contiguous")
-    if out is None:
-        out = _like(q, stream, dev)
-    else:
+    if q.shape != (batch, heads, _lib.HEAD_DIM):
+        _refuse(where, f"q must hold {batch} tokens of {heads} heads of {_lib.HEAD_DIM}")
+    if out is not None:
         _given(out, q.shape, dev, where, "out")
+        if out.data_ptr() % 16:
+            _refuse(where, "out must be aligned to 16 bytes")
     if lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != dev
                             or not lse.is_contiguous()):
         _refuse(where, f"lse must be contiguous fp32 [{batch}, {heads}] on {dev}")
     if scale is None:
         scale = _SCALE
-    elif not (scale > 0 and math.isfinite(scale)):
-        _refuse(where, "scale must be positive and finite")
+    else:
+        scale = ctypes.c_float(scale).value   # as the library takes it
+        if not (scale > 0 and math.isfinite(scale)):
+            _refuse(where, "scale must be positive and finite in 32 bits")
+    return out, lse, scale, window, sinks
+
+
+def _attend(cache, q, ws, out, lse, scale, window, sinks, where, stream):
+    """paged_attend with arguments from _attend_args."""
+    dev = cache.device
+    qp, q_row, q_head = _rows(q, cache.num_heads, dev, where, "q")
+    if q_head != _lib.HEAD_DIM and cache.num_heads > 1:
+        _refuse(where, "the heads of q must be contiguous")
+    if out is None:
+        out = _like(q, stream, dev)
     _run("jfa_paged_attend", dev, stream, cache._ref, qp, q_row, scale, window, sinks, _ws(cache, ws, where),
          out.data_ptr(), None if lse is None else lse.data_ptr())
     return out
@@ -529,9 +554,12 @@ def paged_decode_step(cache: PagedKVCache, q, k, v, positions, plan: RotaryPlan,
     append its key and value, attend.  q bf16 [B, H, 128], k and v bf16
     [B, H_kv, 128] (slices of one projection's output will do), positions
     [B]; the table has grown by one token a sequence (PageTable.grow(1)).
-    Three launches.  Returns out bf16 [B, H, 128]."""
-    if q.shape[0] != cache.table.batch:
-        _refuse("paged_decode_step", f"q must hold {cache.table.batch} tokens")
+    Three launches.  Returns out bf16 [B, H, 128].  A call that is refused has
+    changed nothing; one that ran is not run again at the same lengths (see
+    paged_append)."""
+    where = "paged_decode_step"
+    # what the attention would refuse, before the append writes
+    args = _attend_args(cache, q, out, lse, scale, window, sinks, where)
     q, k = qk_norm_rope(q, k, positions, plan, q_weight, k_weight, eps, stream=stream)
     paged_append(cache, k, v, ws, stream=stream)
-    return paged_attend(cache, q, ws, scale, window, sinks, out, lse, stream=stream)
+    return _attend(cache, q, ws, *args, where, stream)

@@ -601,7 +601,10 @@ int jfa_paged_workspace_bytes(const jfa_paged* cache, size_t* bytes);
  * tokens; of a range longer than its sequence the last seq_lens[b] rows count
  * (a batch padded in front; none of an idle sequence).  Groups that are complete are
  * quantized (jfa_pack_kv's rule) into the table's pages, the rest becomes the
- * tail.  cu: int32 [batch + 1], device.  One launch.  Stream-ordered. */
+ * tail.  cu: int32 [batch + 1], device.  One launch.  Stream-ordered.
+ * Once for each growth of the lengths: a group that completes is packed from
+ * what the tail held, and the tail is overwritten.  A second append at the same
+ * lengths (a warm-up, a call repeated) would pack new rows in place of old. */
 int jfa_paged_append(const jfa_paged* cache, const uint16_t* k_new, int64_t k_tok, int64_t k_head,
                      const uint16_t* v_new, int64_t v_tok, int64_t v_head, const int32_t* cu,
                      int32_t n_total, void* ws, void* stream);

@@ -337,3 +337,36 @@ def test_python_layer_refusals():
         with pytest.raises(JfaError) as e:
             call()
         assert e.value.status == BAD, i
+
+
+def test_refused_decode_step_launches_nothing(monkeypatch):
+    """Whatever a decode step refuses, it refuses before its first launch: the
+    append cannot be taken back."""
+    from bit_kv_cache_jfa_b200 import paged
+    launched = []
+    monkeypatch.setattr(paged, "_run", lambda where, *a: launched.append(where))
+    t = jfa.PageTable(2, 4, 4, device="cpu")
+    t.grow([64, 3])
+    cache = jfa.PagedKVCache(t, 8, 2)
+    ws = jfa.PagedWorkspace(cache)
+    t.grow(1)
+    q, k = torch.zeros(2, 8, 128, dtype=torch.bfloat16), torch.zeros(2, 2, 128, dtype=torch.bfloat16)
+    plan = jfa.RotaryPlan(device="cpu")
+    pos = t.seq_lens - 1
+    flat = torch.zeros(2 * 8 * 128 + 8, dtype=torch.bfloat16)
+    at = 4 if flat.data_ptr() % 16 == 0 else 0
+    for kw in (dict(out=q.float()), dict(out=q[:1]), dict(out=flat[at:at + 2048].view(2, 8, 128)),
+               dict(lse=torch.zeros(2, 4)), dict(lse=torch.zeros(2, 8).double()), dict(window=-1),
+               dict(window=2**31), dict(window=4, sinks=-1), dict(sinks=2**31), dict(window=2.5), dict(scale=0.0),
+               dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=1e-60), dict(scale=1e60)):
+        with pytest.raises((JfaError, TypeError)):
+            jfa.paged_decode_step(cache, q, k, k, pos, plan, ws, **kw)
+        assert "jfa_paged_append" not in launched, kw
+    with pytest.raises(JfaError):
+        jfa.paged_decode_step(cache, q[:, :4], k, k, pos, plan, ws)
+    with pytest.raises(JfaError):
+        jfa.paged_decode_step(cache, q, k, k[:, :1], pos, plan, ws)
+    assert "jfa_paged_append" not in launched
+    launched.clear()
+    jfa.paged_decode_step(cache, q, k, k, pos, plan, ws, scale=0.1, window=5, sinks=1)
+    assert launched == ["jfa_qk_norm_rope", "jfa_paged_append", "jfa_paged_attend"]
