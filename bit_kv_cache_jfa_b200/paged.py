@@ -82,17 +82,34 @@ def _rows(x, heads, dev, where, name):
     return x.data_ptr(), strides[0] if shape[0] > 1 else 0, strides[1] if heads > 1 else 0
 
 
+def _overlap(s0, n0, s1, n1):
+    """Whether any two of the n0 * n1 rows of 128 elements at i s0 + j s1 share one."""
+    if s0 > s1:
+        s0, n0, s1, n1 = s1, n1, s0, n0
+    reach = s0 * (n0 - 1) + 128           # of the rows along the smaller stride
+    if n0 > 1 and s0 < 128:
+        return True
+    if n1 == 1 or s1 >= reach:
+        return False
+    if n0 == 1:
+        return True
+    # rows j apart along s1 are i or i + 1 strides s0 off at the nearest
+    for j in range(1, n1):
+        if j * s1 >= reach:
+            return False
+        i = j * s1 // s0
+        if j * s1 - i * s0 < 128 or (i + 1 < n0 and (i + 1) * s0 - j * s1 < 128):
+            return True
+    return False
+
+
 def _out_rows(x, like, heads, dev, where, name):
     """_rows of an output: its input's shape, no two rows in one place."""
     if x.shape != like.shape:
         _refuse(where, f"{name} must have its input's shape")
     at = _rows(x, heads, dev, where, name)
-    room = 128  # of a row, then of the rows along the smaller stride
-    for stride, count in sorted(((at[1], x.shape[0]), (at[2], heads))):
-        if count > 1:
-            if stride < room:
-                _refuse(where, f"{name} must not overlap itself")
-            room = stride * count
+    if x.numel() and _overlap(at[1], x.shape[0], at[2], heads):
+        _refuse(where, f"{name} must not overlap itself")
     return at
 
 

@@ -42,3 +42,17 @@ def test_refused_decode_step_changes_nothing(bad):
     assert ws.error_flag(cache) == 0
     check_cache(table, cache, [(torch.cat((a, k[b:b + 1].cpu())), torch.cat((c, new[b:b + 1, 6:].cpu())))
                                if lens[b] else (a, c) for b, (a, c) in enumerate(rows)])
+
+
+def test_rotation_in_place_between_other_heads():
+    """Every other head of seven, in place: no two rows share a byte."""
+    plan = jfa.RotaryPlan(128)
+    wide = torch.randn(9, 7, D, generator=gen(85)).bfloat16().cuda()
+    pos = torch.arange(9, device="cuda")
+    before = wide.clone()
+    k = wide[:, 1::2]
+    want = jfa.qk_norm_rope(wide[:, ::2], k, pos, plan)
+    got = jfa.qk_norm_rope(wide[:, ::2], k, pos, plan, q_out=wide[:, ::2], k_out=torch.empty_like(want[1]))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(wide[:, 1::2], before[:, 1::2]) and torch.equal(wide[:, ::2], want[0])

@@ -370,3 +370,33 @@ def test_refused_decode_step_launches_nothing(monkeypatch):
     launched.clear()
     jfa.paged_decode_step(cache, q, k, k, pos, plan, ws, scale=0.1, window=5, sinks=1)
     assert launched == ["jfa_qk_norm_rope", "jfa_paged_append", "jfa_paged_attend"]
+
+
+def test_outputs_overlap_exactly_when_two_rows_share_an_element():
+    from bit_kv_cache_jfa_b200 import paged
+    rng = random.Random(11)
+    seen = [0, 0]
+    for _ in range(3000):
+        n0, n1 = rng.randint(1, 6), rng.randint(1, 6)
+        s0, s1 = (rng.choice([8 * rng.randint(0, 130), 128 * rng.randint(0, 8)]) for _ in range(2))
+        at = sorted(i * s0 + j * s1 for i in range(n0) for j in range(n1))
+        want = any(b - a < 128 for a, b in zip(at, at[1:]))
+        assert paged._overlap(s0, n0, s1, n1) == want, (s0, n0, s1, n1)
+        seen[want] += 1
+    assert min(seen) > 300
+
+
+def test_outputs_between_other_rows_are_taken(monkeypatch):
+    """Every other head of an odd number, heads before tokens, and rows that lie
+    between one another without sharing a byte."""
+    from bit_kv_cache_jfa_b200 import paged
+    monkeypatch.setattr(paged, "_run", lambda *a: None)
+    plan = jfa.RotaryPlan(device="cpu")
+    wide = torch.zeros(6, 7, 128, dtype=torch.bfloat16)
+    pos = torch.zeros(6, dtype=torch.int32)
+    k = torch.zeros(6, 1, 128, dtype=torch.bfloat16)
+    for out in (wide[:, ::2], wide.view(7, 6, 128).transpose(0, 1)[:, :4], wide[:, 1:5]):
+        got, _ = jfa.qk_norm_rope(out, k, pos, plan, q_out=out)
+        assert got is out
+    between = wide.as_strided((2, 4, 128), (384, 256, 1))
+    assert jfa.qk_norm_rope(between, k[:2], pos[:2], plan, q_out=between)[0] is between
