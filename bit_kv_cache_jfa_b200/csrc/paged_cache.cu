@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(kPcThreads) paged_fork_kernel(const __grid_con
     if (tid == 0) set_flag(p.flag, JFA_DEVERR_BAD_INDEX);
     return;
   }
-  const int n = checked_len(p.c.seq_lens[src], p.c.max_pages, p.flag);
+  const int n = p.c.seq_lens[src];
+  if (checked_len(n, p.c.max_pages, p.flag) != n) return;  // the child stays as it is
   const int count = n - split_point(n);
   const size_t hkv = p.c.num_kv_heads;
   const size_t so = ((size_t)src * hkv + h) * kPgTailBytes, d0 = ((size_t)dst * hkv + h) * kPgTailBytes;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import bit_kv_cache_jfa_b200 as jfa
-from bit_kv_cache_jfa_b200 import JfaError
+from bit_kv_cache_jfa_b200 import JfaError, _lib
 from test_gpu_paged import D, check_cache, gen, make, rand_q
 
 pytestmark = pytest.mark.gpu
@@ -56,3 +56,90 @@ def test_rotation_in_place_between_other_heads():
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(wide[:, 1::2], before[:, 1::2]) and torch.equal(wide[:, ::2], want[0])
+
+
+def state(table, cache):
+    return [x.clone() for x in (cache.pages, cache.tail_k, cache.tail_v, table.table, table.seq_lens)]
+
+
+def flag_of(cache, ws):
+    torch.cuda.synchronize()
+    flag = ws.error_flag(cache)
+    ws.clear_error(cache)
+    return flag
+
+
+@pytest.mark.parametrize("n", [-1, -2**31, 2**31 - 1, 64 * 5 + 65])
+def test_fork_of_a_parent_of_bad_length_leaves_the_child(n):
+    """The pair is skipped whole; the call's other pair is made."""
+    lens = [130, 200, 70, 64]
+    table, cache, ws, rows = make(lens, 2, 2, seed=87)      # rows of 5 entries
+    assert table.max_pages == 5
+    table.seq_lens[0] = n
+    before = state(table, cache)
+    jfa.paged_fork(cache, torch.tensor([[0, 1], [2, 3]], dtype=torch.int32).cuda(), ws)
+    assert flag_of(cache, ws) == _lib.DEVERR_BAD_INDEX
+    after = state(table, cache)
+    assert torch.equal(before[0], after[0])
+    for a, b in zip(before[1:], after[1:]):
+        assert torch.equal(a[:3], b[:3])                    # parent, its child, the other parent
+    table.seq_lens[0] = 130
+    table.rows[3], rows[3] = list(table.rows[2]), rows[2]
+    assert int(table.seq_lens[3]) == 70
+    check_cache(table, cache, rows)
+
+
+@pytest.mark.parametrize("pairs", [[[0, 5]], [[-1, 1]], [[0, 0]], [[0, 1], [1, 2]], [[0, 2], [1, 2]],
+                                   [[2**31 - 1, 1]], [[0, -2**31]]])
+def test_refused_forks_change_nothing(pairs):
+    """Pairs that are bad by themselves, or that meet (then each of them), beside a good one."""
+    lens = [130, 200, 0, 64, 30]
+    table, cache, ws, rows = make(lens, 2, 2, seed=89)
+    before = state(table, cache)
+    jfa.paged_fork(cache, torch.tensor(pairs + [[3, 4]], dtype=torch.int32).cuda()[:5], ws)
+    assert flag_of(cache, ws) == _lib.DEVERR_BAD_INDEX
+    after = state(table, cache)
+    assert torch.equal(before[0], after[0])
+    for a, b in zip(before[1:], after[1:]):
+        assert torch.equal(a[:4], b[:4])
+    assert int(table.seq_lens[4]) == 64
+    rows[4] = rows[3]
+    check_cache(table, cache, rows)
+
+
+@pytest.mark.parametrize("cu", [[0, 11, 21, 30], [-1, 5, 15, 25], [16, 5, 15, 25], [0, -3, 10, 20],
+                                [0, 2**31 - 1, 10, 20]])
+def test_refused_ranges_change_nothing(cu):
+    """Row ranges outside their tensors are skipped, in the append and in the
+    read-back; a good one of the same call is brought in."""
+    good = [i for i in range(3) if 0 <= cu[i] <= cu[i + 1] <= 24]
+    lens = [130, 200, 300]
+    table, cache, ws, rows = make(lens, 2, 2, seed=90)
+    before = state(table, cache)
+    c = torch.tensor(cu, dtype=torch.int32).cuda()
+    outs = [torch.full((24, 2, D), 77.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    jfa.paged_gather(cache, c, 24, ws, k_out=outs[0], v_out=outs[1])
+    assert flag_of(cache, ws) == _lib.DEVERR_BAD_INDEX
+    whole = jfa.paged_gather(cache, torch.tensor([0, 130, 330, 630], dtype=torch.int32).cuda(), 630, ws)
+    seen = torch.zeros(24, dtype=torch.bool)
+    first = [0, 130, 330]
+    for i in good:
+        seen[cu[i]:cu[i + 1]] = True
+        for x, w in zip(outs, whole):
+            assert torch.equal(x[cu[i]:cu[i + 1]], w[first[i]:first[i] + cu[i + 1] - cu[i]])
+    assert all((x[~seen.cuda()] == 77).all() for x in outs)
+    # the append of these ranges: the table has grown by each good one's rows
+    counts = [cu[i + 1] - cu[i] if i in good else 0 for i in range(3)]
+    table.grow(counts)
+    before = state(table, cache)
+    k, v = (torch.randn(24, 2, D, generator=gen(s)).bfloat16() for s in (91, 92))
+    jfa.paged_append(cache, k.cuda(), v.cuda(), ws, c)
+    assert flag_of(cache, ws) == _lib.DEVERR_BAD_INDEX
+    after = state(table, cache)
+    for i in range(3):
+        if i in good:
+            rows[i] = tuple(torch.cat((a, x[cu[i]:cu[i + 1]])) for a, x in zip(rows[i], (k, v)))
+        else:
+            assert all(torch.equal(a[i], b[i]) for a, b in zip(before[1:3], after[1:3]))
+    assert torch.equal(before[4], after[4]) and torch.equal(before[3], after[3])
+    check_cache(table, cache, rows)
