@@ -63,13 +63,17 @@ __device__ __forceinline__ GroupParams group_params(float mn, float mx) {
 struct WordIn {
   float x[2][2][2], z[2][2], inv[2][2];
 };
-__device__ __noinline__ uint32_t code_fp64(float x, float z, float s) {
+__device__ __noinline__ uint32_t code_fp64(float x, float z, float s, uint32_t* flag) {
+  if (x != x) {  // the ranges pass over it: code 0, as in jfa_pack_kv, but not unseen
+    set_flag(flag, JFA_DEVERR_NONFINITE_QUANT);
+    return 0u;
+  }
   return quant_code((double)x, (double)z, (double)s, 4);
 }
 // The remainder d - (c + 1/2) s at the border next to the quotient is exact,
 // and so is its sign, where d = x - z is (both ways of undoing it agree); else
 // the fp64 quotient decides.
-__device__ __noinline__ uint32_t word_exact(WordIn in) {
+__device__ __noinline__ uint32_t word_exact(WordIn in, uint32_t* flag) {
   uint32_t word = 0u;
 #pragma unroll
   for (int a = 0; a < 2; ++a)
@@ -82,13 +86,13 @@ __device__ __noinline__ uint32_t word_exact(WordIn in) {
         const float x = in.x[a][e][b], d = x - z, down = floorf(d * inv), rest = fmaf(-(down + 0.5f), s, d);
         uint32_t c = (uint32_t)(int)down;
         c += rest > 0.f || (rest == 0.f && (c & 1u)) ? 1u : 0u;
-        if (!(d + z == x && x - d == z && s > 0.f)) c = code_fp64(x, z, s);
+        if (!(d + z == x && x - d == z && s > 0.f)) c = code_fp64(x, z, s, flag);
         word |= (c & 15u) << (4 * a + 16 * e + 8 * b);
       }
     }
   return word;
 }
-__device__ __forceinline__ uint32_t quant_word(const WordIn& in) {
+__device__ __forceinline__ uint32_t quant_word(const WordIn& in, uint32_t* flag) {
   constexpr float kRound = 12582912.f;
   constexpr uint32_t kBits = 0x4B400000u;
   uint32_t word = 0u;
@@ -103,7 +107,7 @@ __device__ __forceinline__ uint32_t quant_word(const WordIn& in) {
         near |= !(fabsf(fmaf(d, in.inv[a][e], kRound - t)) <= 0.49999f);
         word += __float_as_uint(t) << (4 * a + 16 * e + 8 * b);
       }
-  return near ? word_exact(in) : word - kBits * 0x11111111u;
+  return near ? word_exact(in, flag) : word - kBits * 0x11111111u;
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(kApThreads, 6) paged_append_kernel(const __gri
               in.x[c][1][r] = bf_hi(v);
             }
           }
-          const uint32_t word = quant_word(in);
+          const uint32_t word = quant_word(in, p.flag);
           const int q = q0 + 16 * k;
           if (page_ok)
             *reinterpret_cast<uint32_t*>(rec + off_kc() + (q >> 3) * 1024 + ((q & 7) * 4 + i) * 32 + 4 * w) = word;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kApThreads, 6) paged_append_kernel(const __gri
               in.x[hs][e][c] = gid & 1 ? bf_hi(v) : bf_lo(v);
             }
           }
-        const uint32_t word = quant_word(in);
+        const uint32_t word = quant_word(in, p.flag);
         if (page_ok) *reinterpret_cast<uint32_t*>(at + gid * 64) = word;
       }
     }

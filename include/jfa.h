@@ -570,8 +570,8 @@ int jfa_qk_norm_rope(const jfa_rope* rope, void* stream);
  * lengths outside [0, 64 max_pages + 64], row ranges outside their tensors,
  * bad pairs, and moves outside the pool or against their remap set
  * JFA_DEVERR_BAD_INDEX in the workspace; what they name is skipped.  A
- * non-finite scale or zero point that is packed sets
- * JFA_DEVERR_NONFINITE_QUANT.
+ * non-finite scale or zero point that is packed, or a NaN (which ranges pass
+ * over: its code is 0, as with jfa_pack_kv), sets JFA_DEVERR_NONFINITE_QUANT.
  * ------------------------------------------------------------------------- */
 #define JFA_PAGE_RECORD_BYTES 9728 /* a page of one KV head */
 

@@ -7,7 +7,7 @@ import torch
 
 import bit_kv_cache_jfa_b200 as jfa
 from bit_kv_cache_jfa_b200 import JfaError, _lib
-from test_gpu_paged import D, check_cache, gen, make, rand_q
+from test_gpu_paged import D, check_cache, gen, make, make_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,37 @@ def test_refused_ranges_change_nothing(cu):
             assert all(torch.equal(a[i], b[i]) for a, b in zip(before[1:3], after[1:3]))
     assert torch.equal(before[4], after[4]) and torch.equal(before[3], after[3])
     check_cache(table, cache, rows)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_nan_rows_are_flagged_once_packed(sign):
+    """A NaN in the tail is kept as it is; when its group is packed the flag
+    shows it, its code is 0 and the others' are as without it."""
+    n, hkv = 64, 2
+    nan = torch.tensor([sign * math.nan]).bfloat16()
+    for keys in (True, False):
+        for token, channel in ((0, 0), (5, 77), (63, 127), (31, 64)):
+            table = jfa.PageTable(2, 6, 4)
+            cache = jfa.PagedKVCache(table, hkv, hkv)
+            ws = jfa.PagedWorkspace(cache)
+            k, v = make_rows(2 * n + 2, hkv, 95 + token)
+            clean = (k, v)[0 if keys else 1][:n].clone()
+            # what a code of 0 stands for: the smallest of the others it shares a scale with
+            x = clean[:, 1, channel] if keys else clean[token, 1, channel // 32 * 32:channel // 32 * 32 + 32]
+            others = torch.cat((x[:token], x[token + 1:])) if keys else \
+                torch.cat((x[:channel % 32], x[channel % 32 + 1:]))
+            (k, v)[0 if keys else 1][token, 1, channel] = nan
+            clean[token, 1, channel] = others.min()
+            jfa.paged_append(cache, k[:2 * n].cuda(), v[:2 * n].cuda(), ws, table.grow([n, n]))
+            assert flag_of(cache, ws) == 0, "in the tail"
+            assert torch.isnan(cache.tail_k if keys else cache.tail_v).sum() == 1
+            table.grow(1)
+            jfa.paged_append(cache, k[2 * n:].cuda(), v[2 * n:].cuda(), ws)
+            assert flag_of(cache, ws) == _lib.DEVERR_NONFINITE_QUANT
+            rows = []
+            for b in range(2):
+                kk, vv = k[n * b:n * b + n], v[n * b:n * b + n]
+                if b == 0:
+                    kk, vv = (clean, vv) if keys else (kk, clean)
+                rows.append((torch.cat((kk, k[2 * n + b:][:1])), torch.cat((vv, v[2 * n + b:][:1]))))
+            check_cache(table, cache, rows)
