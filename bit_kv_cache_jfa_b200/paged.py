@@ -46,6 +46,8 @@ def _run(where, dev, stream, *args):
     """Call the library's ``where`` on dev and ``stream``.  These calls take
     microseconds on the device: what the host adds is kept small (one look at
     the current device and stream, no context manager when dev is current)."""
+    if dev.index is None:
+        _refuse(where, f"needs a CUDA device, not {dev}")
     fn = _calls.get(where)
     if fn is None:
         fn = _calls[where] = getattr(_lib.load(), where)
@@ -115,6 +117,8 @@ def _out_rows(x, like, heads, dev, where, name):
 
 def _fresh(make, stream, dev):
     """make(), an output, from the memory of the call's stream."""
+    if dev.index is None:
+        _refuse("stream", f"needs a CUDA device, not {dev}")
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev)
     with torch.cuda.stream(stream):
@@ -426,6 +430,8 @@ class PagedWorkspace:
         self.sizes = (cache.table.batch, cache.num_kv_heads)
 
     def error_flag(self, cache: PagedKVCache, stream=None) -> int:
+        if cache.device.index is None:
+            _refuse("jfa_paged_check_error", f"needs a CUDA device, not {cache.device}")
         with torch.cuda.device(cache.device):
             status, flag = _lib.jfa_paged_check_error(cache.struct(), self.buf, _handle(cache.device, stream))
         if status != _lib.JFA_ERR_DEVICE:

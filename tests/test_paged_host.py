@@ -400,3 +400,26 @@ def test_outputs_between_other_rows_are_taken(monkeypatch):
         assert got is out
     between = wide.as_strided((2, 4, 128), (384, 256, 1))
     assert jfa.qk_norm_rope(between, k[:2], pos[:2], plan, q_out=between)[0] is between
+
+
+def test_calls_on_host_tensors_are_refused():
+    """The book of a table without a device works; the calls name what is missing."""
+    t = jfa.PageTable(2, 4, 4, device="cpu")
+    cu = t.grow([64, 3])
+    cache = jfa.PagedKVCache(t, 8, 2)
+    ws = jfa.PagedWorkspace(cache)
+    rows, q = torch.zeros(67, 2, 128, dtype=torch.bfloat16), torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    plan = jfa.RotaryPlan(device="cpu")
+    pos = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda **kw: jfa.paged_append(cache, rows, rows, ws, cu, **kw),
+                 lambda **kw: jfa.paged_gather(cache, cu, 67, ws, **kw),
+                 lambda **kw: jfa.paged_attend(cache, q, ws, **kw),
+                 lambda **kw: jfa.paged_fork(cache, torch.zeros(1, 2, dtype=torch.int32), ws, **kw),
+                 lambda **kw: jfa.paged_move(cache, torch.zeros(1, 2, dtype=torch.int32), ws, **kw),
+                 lambda **kw: jfa.qk_norm_rope(q, rows[:2], pos, plan, **kw),
+                 lambda **kw: jfa.paged_decode_step(cache, q, rows[:2], rows[:2], pos, plan, ws, **kw),
+                 lambda **kw: ws.error_flag(cache, **kw), lambda **kw: ws.clear_error(cache, **kw)):
+        for kw in ({}, dict(stream=256)):
+            with pytest.raises(JfaError) as e:
+                call(**kw)
+            assert e.value.status == BAD and "CUDA" in str(e.value)
