@@ -29,6 +29,7 @@ from ._lib import JFA_ERR_INVALID_ARG, JfaError, Paged, Rope, check
 
 _BF16 = torch.bfloat16
 _SCALE = 1.0 / math.sqrt(_lib.HEAD_DIM)
+_INT_MAX = 2**31 - 1   # the library's counts are of 32 bits
 
 
 def _refuse(where: str, why: str):
@@ -78,8 +79,9 @@ def _rows(x, heads, dev, where, name):
     """Address and strides of bf16 rows [T][heads][128]."""
     shape, strides = x.shape, x.stride()
     if x.dtype != _BF16 or len(shape) != 3 or shape[1] != heads or shape[2] != 128 or x.device != dev \
-            or (strides[2] != 1 and x.numel()):
-        _refuse(where, f"{name} must be bf16 [tokens, {heads}, {_lib.HEAD_DIM}] on {dev}, channels contiguous")
+            or (strides[2] != 1 and x.numel()) or shape[0] > _INT_MAX:
+        _refuse(where, f"{name} must be bf16 [tokens, {heads}, {_lib.HEAD_DIM}] on {dev}, channels contiguous, "
+                       "of fewer than 2^31 tokens")
     # the stride of a dimension of one element means nothing
     return x.data_ptr(), strides[0] if shape[0] > 1 else 0, strides[1] if heads > 1 else 0
 
@@ -265,8 +267,8 @@ class PageTable:
     Updates are enqueued on torch's current stream."""
 
     def __init__(self, batch: int, n_pages: int, max_pages: int, device="cuda"):
-        if not 1 <= batch <= _lib.MAX_BATCH or n_pages < 1 or max_pages < 1:
-            _refuse("PageTable", f"batch must be 1..{_lib.MAX_BATCH}, n_pages and max_pages at least 1")
+        if not 1 <= batch <= _lib.MAX_BATCH or not 1 <= n_pages <= _INT_MAX or not 1 <= max_pages <= _INT_MAX:
+            _refuse("PageTable", f"batch must be 1..{_lib.MAX_BATCH}, n_pages and max_pages 1 or more, and below 2^31")
         self.batch, self.n_pages, self.max_pages = batch, n_pages, max_pages
         self.device = _device(device)
         self.table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=self.device)
@@ -396,6 +398,8 @@ class PagedKVCache:
     def __init__(self, table: PageTable, num_heads: int, num_kv_heads: int):
         self.table, self.device = table, table.device
         self.num_heads, self.num_kv_heads = num_heads, num_kv_heads
+        if max(num_heads, num_kv_heads) > _INT_MAX:
+            _refuse("PagedKVCache", "num_heads and num_kv_heads must be below 2^31")
         # sizes first: a bad geometry is refused before anything is allocated
         self._struct = Paged(table.batch, num_heads, num_kv_heads, table.n_pages, table.max_pages)
         self.workspace_bytes = _lib.jfa_paged_workspace_bytes(self._struct)
@@ -476,8 +480,8 @@ def paged_gather(cache: PagedKVCache, cu, total: int, ws: PagedWorkspace, start=
     where = "paged_gather"
     dev, batch = cache.device, cache.table.batch
     shape = (total, cache.num_kv_heads, _lib.HEAD_DIM)
-    if total < 0:
-        _refuse(where, "total must not be negative")
+    if not 0 <= total <= _INT_MAX:
+        _refuse(where, "total must be 0 or more, and below 2^31")
     if k_out is None:
         k_out = cache.tail_k.new_empty(shape) if stream is None else \
             _fresh(lambda: cache.tail_k.new_empty(shape), stream, dev)

@@ -423,3 +423,27 @@ def test_calls_on_host_tensors_are_refused():
             with pytest.raises(JfaError) as e:
                 call(**kw)
             assert e.value.status == BAD and "CUDA" in str(e.value)
+
+
+def test_counts_past_32_bits_are_refused(monkeypatch):
+    """They would wrap: an append of 2^32 rows (of one row's memory) did nothing."""
+    from bit_kv_cache_jfa_b200 import paged
+    monkeypatch.setattr(paged, "_run", lambda *a: None)
+    t = jfa.PageTable(2, 4, 4, device="cpu")
+    cache = jfa.PagedKVCache(t, 8, 2)
+    ws = jfa.PagedWorkspace(cache)
+    cu = torch.zeros(3, dtype=torch.int32)
+    plan = jfa.RotaryPlan(device="cpu")
+    row, pos = torch.zeros(1, 2, 128, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    some = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    for n in (2**31, 2**32, 2**32 + 4):
+        many = row.expand(n, 2, 128)
+        for call in (lambda: jfa.paged_append(cache, many, many, ws, cu), lambda: jfa.paged_append(cache, many, many, ws),
+                     lambda: jfa.paged_gather(cache, cu, n, ws, k_out=some, v_out=some),
+                     lambda: jfa.qk_norm_rope(many, many, pos.expand(n), plan, q_out=some, k_out=some),
+                     lambda: jfa.PageTable(2, n, 4, device="cpu"), lambda: jfa.PageTable(2, 4, n, device="cpu"),
+                     lambda: jfa.PagedKVCache(t, n, 2), lambda: jfa.PagedKVCache(t, n, n)):
+            with pytest.raises(JfaError) as e:
+                call()
+            assert e.value.status == BAD
+    jfa.paged_append(cache, row.expand(2**31 - 1, 2, 128), row.expand(2**31 - 1, 2, 128), ws, cu)
