@@ -188,6 +188,8 @@ class RotaryPlan:
             _refuse(where, "high_freq_factor must be above low_freq_factor")
         if scaling == "yarn" and not beta_fast > beta_slow > 0:
             _refuse(where, "beta_fast must be above beta_slow, and that above 0")
+        if scaling == "yarn" and not all(math.isfinite(x) for x in (base, original, beta_fast)):
+            _refuse(where, "base, original and beta_fast must be finite")
         self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
         half = rotary_dim // 2
         f = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
@@ -207,10 +209,12 @@ class RotaryPlan:
             ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(half)]
             f = [x * (1 - u + u / factor) for x, u in zip(f, ramp)]
             m = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+        if not all(math.isfinite(x * 2.0**64) for x in f):
+            _refuse(where, "frequencies must be finite, and below 2^960")
         self.frequencies = tuple(f)          # radians per position
         self.amplitude = float(m if amplitude is None else amplitude)
-        if not math.isfinite(self.amplitude):
-            _refuse(where, "amplitude must be finite")
+        if not math.isfinite(ctypes.c_float(self.amplitude).value):
+            _refuse(where, "amplitude must be finite in 32 bits")
         turns = [round(x / (2 * math.pi) * 2.0**64) % 2**64 for x in f]   # in 2^-64 turns
         self.freq = torch.tensor([t - 2**64 if t >= 2**63 else t for t in turns], dtype=torch.int64,
                                  device=_device(device))

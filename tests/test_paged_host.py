@@ -447,3 +447,22 @@ def test_counts_past_32_bits_are_refused(monkeypatch):
                 call()
             assert e.value.status == BAD
     jfa.paged_append(cache, row.expand(2**31 - 1, 2, 128), row.expand(2**31 - 1, 2, 128), ws, cu)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(scaling="linear", factor=1e-320), dict(scaling="linear", factor=1e-300), dict(base=math.nan),
+    dict(scaling="yarn", original=math.inf, factor=2.0), dict(scaling="yarn", original=8192, base=math.inf),
+    dict(scaling="llama3", original=8192, low_freq_factor=-math.inf),
+    dict(scaling="yarn", original=8192, beta_fast=math.inf), dict(scaling="llama3", original=math.nan),
+    dict(amplitude=1e39), dict(amplitude=-1e300), dict(amplitude=math.nan)], ids=str)
+def test_rotary_plan_refuses_what_no_frequency_comes_of(kw):
+    with pytest.raises(JfaError) as e:
+        jfa.RotaryPlan(device="cpu", **kw)
+    assert e.value.status == BAD
+
+
+def test_rotary_plan_of_extreme_factors():
+    """Frequencies of many turns a position are whole numbers of 2^-64 turns as well."""
+    plan = jfa.RotaryPlan(4, base=10000.0, scaling="linear", factor=1e-200, device="cpu")
+    assert plan.frequencies[0] == 1 / 1e-200
+    assert jfa.RotaryPlan(4, scaling="linear", factor=1e300, device="cpu").freq.tolist() == [0, 0]
