@@ -43,6 +43,8 @@
 // comes into [2^-3, 2): where x > 0 it goes to the scales (exactly), else to
 // the weights of that group (past fp16 otherwise), so that small values lose
 // no more, and large ones cost the groups beside them nothing.
+#include <float.h>
+
 #include "jfa_approx.cuh"
 #include "jfa_paged.cuh"
 
@@ -86,8 +88,8 @@ constexpr float kPaRoom = 5.f;
 constexpr int kPaSlack = 3;
 constexpr float kPaLn2 = 0.6931471805599453f;
 // Where a reference starts: finite, so that a masked logit (-inf) minus it is
-// -inf and its weight 0.
-constexpr float kPaMin = -1e30f;
+// -inf and its weight 0, and below every logit.
+constexpr float kPaMin = -FLT_MAX;
 
 struct PagedAttendParams {
   jfa_paged c;

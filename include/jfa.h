@@ -621,7 +621,8 @@ int jfa_paged_gather(const jfa_paged* cache, const int32_t* cu, const int32_t* s
  * over its cache: softmax over the visible tokens of scale q_h . k_t, applied
  * to v_t.  Visible: every token, or with window > 0 those with
  * t >= seq_lens[b] - window or t < sinks.  q: bf16 [batch][H][128], rows
- * q_row elements apart (a multiple of 8, heads contiguous).  out: bf16
+ * q_row elements apart (a multiple of 8, heads contiguous), below 2^100 in
+ * magnitude (logits and their factors are of 32 bits).  out: bf16
  * [batch][H][128] contiguous, zeros for an idle sequence; lse (may be null):
  * fp32 [batch][H], the natural logarithm of the sum of exp(scale q.k), -inf
  * for an idle one.  One launch.  Stream-ordered. */

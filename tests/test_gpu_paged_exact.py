@@ -140,3 +140,30 @@ def test_mass_spread_over_many_tokens_far_below_one(size, loud):
         assert np.linalg.norm(got[b] - out) <= RMS * np.linalg.norm(out), b
         assert (np.abs(got[b] - out) <= bound).all(), b
         assert (np.abs(lse[b].cpu().double().numpy() - l) <= l_bound).all(), b
+
+
+@pytest.mark.parametrize("q_value", [-2.0**97, -2.0**99, 2.0**99, -2.0**60, 0.0])
+def test_logits_of_any_size(q_value):
+    """Equal logits far below and above zero: the mean of the values.  Keys of 1
+    and powers of two, so that every logit is the same number exactly."""
+    lens = [200, 1, 64, 1000]
+    table = jfa.PageTable(len(lens), 30, 17)
+    cache = jfa.PagedKVCache(table, 4, 2)
+    ws = jfa.PagedWorkspace(cache)
+    _, v = make_rows(sum(lens), 2, 99)
+    jfa.paged_append(cache, torch.ones_like(v).cuda(), v.cuda(), ws, table.grow(lens))
+    lse = torch.zeros(len(lens), 4, device="cuda")
+    out = jfa.paged_attend(cache, torch.full((len(lens), 4, D), q_value).bfloat16().cuda(), ws, lse=lse)
+    torch.cuda.synchronize()
+    assert ws.error_flag(cache) == 0
+    at = 0
+    for b, n in enumerate(lens):
+        ref = Ref(torch.ones(n, 2, D).bfloat16(), v[at:at + n])
+        at += n
+        want = np.repeat(ref.v.mean(1), 2, 0)
+        # 1 / n of each: the value's sum in 32 bits, its product with fp16 weights
+        # exact or rounded once, the mass; bf16 at the end
+        size = np.repeat(np.abs(ref.v).max(1), 2, 0)
+        assert (np.abs(out[b].cpu().double().numpy() - want) <= BF16 * np.abs(want) + 2.0**-10 * 3 * size).all()
+        x = q_value * D / math.sqrt(D)
+        assert (np.abs(lse[b].cpu().double().numpy() - (x + math.log(n))) <= 2.0**-20 * (abs(x) + 8)).all()
