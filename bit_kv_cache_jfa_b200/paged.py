@@ -229,7 +229,8 @@ def qk_norm_rope(q, k, positions, plan: RotaryPlan, q_weight=None, k_weight=None
     q bf16 [T, H, 128], k bf16 [T, H_kv, 128] (any token and head strides that
     are multiples of 8, channels contiguous); positions int32 or int64 [T];
     weights bf16 [128].  Returns (q, k) bf16, contiguous unless given; q_out=q
-    and k_out=k work in place."""
+    and k_out=k work in place, and otherwise an output may overlap neither an
+    input nor the other output."""
     where = "qk_norm_rope"
     dev = plan.freq.device
     qs, ks = q.shape, k.shape
@@ -495,6 +496,8 @@ def paged_gather(cache: PagedKVCache, cu, total: int, ws: PagedWorkspace, start=
         v_out = _like(k_out, stream, dev)
     else:
         _given(v_out, shape, dev, where, "v_out")
+    if abs(k_out.data_ptr() - v_out.data_ptr()) < 2 * k_out.numel():
+        _refuse(where, "k_out and v_out must not overlap")
     cup = _int32(cu, batch + 1, dev, where, "cu")
     stp = None if start is None else _int32(start, batch, dev, where, "start")
     _run("jfa_paged_gather", dev, stream, cache._ref, cup, stp, total, k_out.data_ptr(), v_out.data_ptr(),
@@ -508,8 +511,9 @@ def paged_attend(cache: PagedKVCache, q, ws: PagedWorkspace, scale=None, window:
     (window > 0) over the last ``window`` of them and the first ``sinks``.
 
     q: bf16 [B, H, 128] (heads contiguous, any row stride that is a multiple
-    of 8).  Returns out bf16 [B, H, 128], zeros for an idle sequence; lse (fp32
-    [B, H], if given) gets the natural logarithm of the softmax's sum."""
+    of 8).  Returns out bf16 [B, H, 128] (which may be q), zeros for an idle
+    sequence; lse (fp32 [B, H], if given) gets the natural logarithm of the
+    softmax's sum."""
     where = "paged_attend"
     args = _attend_args(cache, q, out, lse, scale, window, sinks, where)
     return _attend(cache, q, ws, *args, where, stream)

@@ -612,8 +612,8 @@ int jfa_paged_append(const jfa_paged* cache, const uint16_t* k_new, int64_t k_to
 /* Read rows back as bf16 (dequantized where packed, else the exact rows):
  * tokens start[b] .. start[b] + cu[b + 1] - cu[b] - 1 of sequence b (start
  * null: from 0) into rows [cu[b], cu[b + 1]) of k_out / v_out [n_total][H_kv]
- * [128]; other rows are left as they are.  cu int32 [batch + 1], start int32
- * [batch], device.  One launch.  Stream-ordered. */
+ * [128], which do not overlap; other rows are left as they are.  cu int32
+ * [batch + 1], start int32 [batch], device.  One launch.  Stream-ordered. */
 int jfa_paged_gather(const jfa_paged* cache, const int32_t* cu, const int32_t* start,
                      int32_t n_total, uint16_t* k_out, uint16_t* v_out, void* ws, void* stream);
 
@@ -623,7 +623,8 @@ int jfa_paged_gather(const jfa_paged* cache, const int32_t* cu, const int32_t* s
  * t >= seq_lens[b] - window or t < sinks.  q: bf16 [batch][H][128], rows
  * q_row elements apart (a multiple of 8, heads contiguous), below 2^100 in
  * magnitude (logits and their factors are of 32 bits).  out: bf16
- * [batch][H][128] contiguous, zeros for an idle sequence; lse (may be null):
+ * [batch][H][128] contiguous (it may be q, if that is contiguous too, and
+ * overlaps nothing else), zeros for an idle sequence; lse (may be null):
  * fp32 [batch][H], the natural logarithm of the sum of exp(scale q.k), -inf
  * for an idle one.  One launch.  Stream-ordered. */
 int jfa_paged_attend(const jfa_paged* cache, const uint16_t* q, int64_t q_row, float scale,

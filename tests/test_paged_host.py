@@ -466,3 +466,20 @@ def test_rotary_plan_of_extreme_factors():
     plan = jfa.RotaryPlan(4, base=10000.0, scaling="linear", factor=1e-200, device="cpu")
     assert plan.frequencies[0] == 1 / 1e-200
     assert jfa.RotaryPlan(4, scaling="linear", factor=1e300, device="cpu").freq.tolist() == [0, 0]
+
+
+def test_read_back_into_one_place_is_refused(monkeypatch):
+    from bit_kv_cache_jfa_b200 import paged
+    monkeypatch.setattr(paged, "_run", lambda *a: None)
+    t = jfa.PageTable(2, 4, 4, device="cpu")
+    cache = jfa.PagedKVCache(t, 8, 2)
+    ws = jfa.PagedWorkspace(cache)
+    cu = torch.zeros(3, dtype=torch.int32)
+    both = torch.zeros(10, 2, 128, dtype=torch.bfloat16)
+    for k, v in ((both[:5], both[:5]), (both[:5], both[4:9]), (both[4:9], both[:5])):
+        with pytest.raises(JfaError) as e:
+            jfa.paged_gather(cache, cu, 5, ws, k_out=k, v_out=v)
+        assert e.value.status == BAD
+    jfa.paged_gather(cache, cu, 5, ws, k_out=both[:5], v_out=both[5:])
+    jfa.paged_gather(cache, cu, 5, ws, k_out=both[5:], v_out=both[:5])
+    jfa.paged_gather(cache, cu, 0, ws)
