@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import bit_kv_cache_jfa_b200 as jfa
-from test_gpu_paged import BF16, D, Ref, gen, make_rows
+from test_gpu_paged import BF16, D, Ref, gen, make, make_rows, rand_q
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +167,51 @@ def test_logits_of_any_size(q_value):
         assert (np.abs(out[b].cpu().double().numpy() - want) <= BF16 * np.abs(want) + 2.0**-10 * 3 * size).all()
         x = q_value * D / math.sqrt(D)
         assert (np.abs(lse[b].cpu().double().numpy() - (x + math.log(n))) <= 2.0**-20 * (abs(x) + 8)).all()
+
+
+@pytest.mark.parametrize("fill", [0xFFFF, 0x7C00, 0x7BFF, 0x7000, 0x3C00, 0x0001])
+@pytest.mark.parametrize("window,sinks", [(100, 5), (100, 0), (1, 70), (130, 64), (65, 129)])
+def test_masked_values_change_no_bit(fill, window, sinks):
+    """Value scales and zero points of masked tokens, in groups that are seen in
+    part: NaN, infinite, the largest numbers, large and small ones."""
+    lens = [200, 333, 70, 64, 600]
+    table, cache, ws, rows = make(lens, 4, 2, seed=101)
+    q = rand_q(5, 4, 101).cuda()
+    want = jfa.paged_attend(cache, q, ws, window=window, sinks=sinks).clone()
+    tab, pages = table.table.cpu(), cache.pages.clone().cpu()
+    changed = 0
+    for b, n in enumerate(lens):
+        for t in range(64 * ((n - 1) // 64)):
+            if sinks <= t < n - window:
+                s = t % 64
+                for j in range(4):
+                    at = 4608 + s // 16 * 128 + s % 8 // 2 * 32 + j * 8 + s % 16 // 8 * 4 + 2 * (s % 2)
+                    for part in (at, at + 512):
+                        pages[int(tab[b, t // 64]), :, part] = fill & 0xFF
+                        pages[int(tab[b, t // 64]), :, part + 1] = fill >> 8
+                changed += 1
+    assert changed > 100
+    cache.pages.copy_(pages)
+    lse = torch.zeros(5, 4, device="cuda")
+    got = jfa.paged_attend(cache, q, ws, window=window, sinks=sinks, lse=lse)
+    torch.cuda.synchronize()
+    assert ws.error_flag(cache) == 0
+    assert torch.equal(got, want) and torch.isfinite(lse).all()
+
+
+def test_read_back_to_16_byte_aligned_rows():
+    """Outputs that begin 16 bytes past a 32-byte border, or one of them."""
+    lens = [200, 0, 129, 64]
+    table, cache, ws, rows = make(lens, 3, 3, seed=103)
+    cu = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32).cuda()
+    total = sum(lens)
+    want = jfa.paged_gather(cache, cu, total, ws)
+    for offs in ((8, 8), (8, 0), (0, 8), (24, 16)):
+        flat = [torch.full((total * 3 * D + 64,), 77.0, dtype=torch.bfloat16, device="cuda") for _ in offs]
+        outs = [f[o:o + total * 3 * D].view(total, 3, D) for f, o in zip(flat, offs)]
+        jfa.paged_gather(cache, cu, total, ws, k_out=outs[0], v_out=outs[1])
+        torch.cuda.synchronize()
+        assert ws.error_flag(cache) == 0
+        for f, o, x, w in zip(flat, offs, outs, want):
+            assert torch.equal(x, w)
+            assert (f[:o] == 77).all() and (f[o + total * 3 * D:] == 77).all()
