@@ -508,9 +508,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     auto visible = [&](int t) {
       return !(kind & kItSkip) && t < rv.n && (t >= rv.win_lo || t < rv.sink_end);
     };
-    if (!ready) failed |= !mbar_wait_bounded(&bar_k[st], (par_k >> st) & 1u);
+    failed = !__all_sync(0xFFFFFFFFu, ready || mbar_wait_bounded(&bar_k[st], (par_k >> st) & 1u));
+    if (failed) break;
     par_k ^= 1u << st;
-    __syncwarp();
     const uint8_t* rk = ring + st * kPaK;
     const uint8_t* rvb = ring + 2 * kPaK;
     if (!(kind & kItTail)) {
@@ -601,9 +601,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         pa[mt] = movmatrix_trans(pack_h2(approx_weight(u[mt][0], m_run[0]), approx_weight(u[mt][1], m_run[1])));
         pb[mt] = movmatrix_trans(pack_h2(approx_weight(u[mt][2], m_run[0]), approx_weight(u[mt][3], m_run[1])));
       }
-      if (!there) failed |= !mbar_wait_bounded(bar_v, par_v);
+      failed = !__all_sync(0xFFFFFFFFu, there || mbar_wait_bounded(bar_v, par_v));
+      if (failed) break;
       par_v ^= 1u;
-      __syncwarp();
       ready = i + 1 < i1 && mbar_try_wait(&bar_k[st ^ 1], (par_k >> (st ^ 1)) & 1u);
       if (kind & kItMask) {
         // What a masked token holds does not matter, infinities too: its scales
@@ -701,9 +701,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
         ph[x] = movmatrix_trans(hi);
         pl[x] = movmatrix_trans(pack_b2(w0 - bf_lo(hi), w1 - bf_hi(hi)));
       }
-      if (!there) failed |= !mbar_wait_bounded(bar_v, par_v);
+      failed = !__all_sync(0xFFFFFFFFu, there || mbar_wait_bounded(bar_v, par_v));
+      if (failed) break;
       par_v ^= 1u;
-      __syncwarp();
       ready = i + 1 < i1 && mbar_try_wait(&bar_k[st ^ 1], (par_k >> (st ^ 1)) & 1u);
       const uint32_t one = gid == 4 ? 0x3F803F80u : 0u;
       mma_bf16(dz, one, 0u, one, 0u, ph[0], ph[1]);
@@ -738,7 +738,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
       store_partial(reinterpret_cast<float*>(ring));  // every copy has been used
     }
   }
-  if (failed) set_flag(p.flag, JFA_DEVERR_TIMEOUT);
+  if (failed) {  // give up: the copies that may be in flight, once more (bounded)
+    set_flag(p.flag, JFA_DEVERR_TIMEOUT);
+    mbar_wait_bounded(&bar_k[0], par_k & 1u);
+    mbar_wait_bounded(&bar_k[1], par_k >> 1);
+    mbar_wait_bounded(bar_v, par_v);
+  }
   if (lane == 0) {
     tail_seg[warp] = my_tail_seg;
     head_seg[warp] = my_head_seg;
