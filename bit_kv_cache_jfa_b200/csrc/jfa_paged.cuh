@@ -25,6 +25,14 @@ static_assert(kPgRec == 512 + 4096 + 1024 + 4096, "K4V4 record");
 // Byte offset of chunk c (16 bytes) of tail slot t inside its (sequence, KV head).
 JFA_HD int tail_chunk(int t, int c) { return t * kPgRow + ((c ^ (t & 7)) << 4); }
 
+// A pair of bf16 numbers: its values, and the pair of two values.
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
 // Workspace: the error flag, a ticket per (sequence, KV head) (zero between
 // calls) and the attention's partials: two per CTA, and one per warp.
 constexpr int kPgMaxCtas = 192;

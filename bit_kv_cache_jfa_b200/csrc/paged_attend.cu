@@ -197,12 +197,6 @@ __device__ __forceinline__ uint32_t h2_rest(uint32_t a, uint32_t b, uint32_t c) 
                             __hneg2(*reinterpret_cast<__half2*>(&c)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // 16-bit halves kept for the visible ones of two tokens.
 __device__ __forceinline__ uint32_t half_mask(bool lo, bool hi) {
   return (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
@@ -697,9 +691,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float w0 = approx_weight(u[2 * x], m_run[0]), w1 = approx_weight(u[2 * x + 1], m_run[1]);
-        const uint32_t hi = pack_b2(w0, w1);
+        const uint32_t hi = pack_bf2(w0, w1);
         ph[x] = movmatrix_trans(hi);
-        pl[x] = movmatrix_trans(pack_b2(w0 - bf_lo(hi), w1 - bf_hi(hi)));
+        pl[x] = movmatrix_trans(pack_bf2(w0 - bf_lo(hi), w1 - bf_hi(hi)));
       }
       failed = !__all_sync(0xFFFFFFFFu, there || mbar_wait_bounded(bar_v, par_v));
       if (failed) break;
@@ -769,7 +763,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const size_t at = (size_t)row * H + head * G + h;
     *reinterpret_cast<uint2*>(p.out + at * kD + 4 * lane) =
-        make_uint2(pack_b2(O.x * inv, O.y * inv), pack_b2(O.z * inv, O.w * inv));
+        make_uint2(pack_bf2(O.x * inv, O.y * inv), pack_bf2(O.z * inv, O.w * inv));
     if (lane == 0 && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPaLn2;
   };
   {

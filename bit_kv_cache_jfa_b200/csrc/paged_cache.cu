@@ -109,8 +109,6 @@ __device__ __forceinline__ uint32_t quant_word(const WordIn& in, uint32_t* flag)
       }
   return near ? word_exact(in, flag) : word - kBits * 0x11111111u;
 }
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -411,11 +409,6 @@ struct PagedGatherParams {
   uint32_t* flag;
   int n_total;
 };
-
-__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
 
 // Eight codes of a word, shifted so that a byte of it holds the codes of two
 // scales: bits 0-3 with scale s, 4-7 with 16 s (given as s / 16, exact).

@@ -28,18 +28,12 @@ __device__ __forceinline__ void unpack8(uint4 w, float* x) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    x[2 * i] = bf_lo(u[i]);
+    x[2 * i + 1] = bf_hi(u[i]);
   }
 }
 __device__ __forceinline__ uint4 pack8(const float* x) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    o[i] = *reinterpret_cast<uint32_t*>(&v);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  return make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
 }
 
 // A warp per unit: eight heads of one token, four at a time, 8 lanes a head.
