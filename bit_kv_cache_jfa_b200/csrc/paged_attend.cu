@@ -9,11 +9,14 @@
 //
 // What bounds it: the cache is read once, 152 B per packed token and KV head,
 // for 4 * 128 * G flop, far under the tensor rate: HBM, if the SM keeps up
-// with unpacking 4-bit codes.  It keeps up to about 85 % of HBM's rate while it
-// streams (917 instructions a record, 475 of them on the half-rate logic
-// pipe); the start and the merges add 10 us: 16 sequences of 32768 tokens, 4 KV
-// heads of 8 query heads, 59.9 us (floor 46.7), one of 131072 tokens, 8 KV
-// heads, 36.7 us (24.3).  So the codes never leave the registers of the
+// with unpacking 4-bit codes (1021 instructions a record, 503 of them on the
+// half-rate logic pipe, 108 MMAs).  By the growth of a call with its length
+// (32768 to 65536 tokens of 16 sequences, 4 KV heads of 8 query heads; 131072
+// to 262144 of one, 8 KV heads of 4) it streams 5.8 and 6.4 TB/s, 88 and 98 %
+// of the copy rate; 16 to 18 us a call do not grow: launch, the chain to the
+// first keys (5 us), warps that end apart (8 us), merges (4 to 7 us).  16
+// sequences of 30001 to 32768 tokens take 66.6 us (floor 46.7), one of 131072
+// 40.8 us (24.3).  So the codes never leave the registers of the
 // warp that loads them: they are stored in the order of the mma.sync
 // fragments, one AND turns a 32-bit word into a ready fp16 operand (subnormal
 // code * 2^(pos - 24), exact), and the scales go to the other operand:
@@ -26,11 +29,12 @@
 // for what falls under fp16's smallest step, 2^-25 of 8 max |q|): a logit is
 // as exact as its 32-bit sums, whatever the range of the keys.  With hi alone
 // its error grows with that range (0.07 where a channel is a hundred times
-// the others' size and the query four times), for 6 % of the time less: 60.0
-// against 64.2 us, 16 sequences of 32768 tokens, 4 KV heads of 8 query heads.
+// the others' size and the query four times), for 7 % of the time less (60.0
+// against 64.2 us, 16 sequences of 32768 tokens, 4 KV heads of 8 query heads).
 // The weights are fp16, and so is a weight times its value's scale: 2^-11 at
-// most each, 3e-4 of an output at unit-normal data against the 1.6e-3 of its
-// bf16, and no more at any other; further halves would double the value MMAs.
+// most each of a token's share, whatever keys and values are (3e-4 of an output
+// at unit-normal data, against the 1.6e-3 of its bf16); the mass is summed from
+// the rounded weights.  Further halves would double the value MMAs.
 // The query is scaled by a power of two to [1/8, 1/4) first, so that q s,
 // times the 16 of the codes' position, stays in fp16's range at every scale a
 // record can hold (131008 / 15).  The weights are taken against a reference
@@ -55,24 +59,25 @@ constexpr int kPaK = 512 + 4096;   // key scales, zero points and codes
 constexpr int kPaV = 1024 + 4096;  // the same of the values
 // Per warp two key buffers and one value buffer: while the values of a group
 // are used the next keys have arrived, and while keys are used the values
-// arrive.  A third key buffer makes it 3 % slower: a warp does not wait for
-// copies once the first have come (130 of its 4500 cycles a group).
+// arrive.  A third key buffer made it 3 % slower: a warp does not wait for
+// copies once the first have come (130 of its 4500 cycles a group, before the
+// keys had a second product).
 constexpr int kPaWarpBytes = 2 * kPaK + kPaV;
 constexpr int kPaSmem = kPgWarps * kPaWarpBytes;
 constexpr int kPaTailTok = 16;                      // tokens of a tail item
 constexpr int kPaTailBytes = kPaTailTok * kPgRow;   // of K or V
 // Items per CTA, at least: few CTAs leave warps alone on their scheduler, many
 // leave more partials to merge over CTAs (2.5 us where there is one).  4 against
-// 8: one sequence of 1000 / 4000 tokens, 8 KV heads, 9.9 / 10.2 and 11.2 / 10.5
-// us; 32 of 200, 8.5 and 10.0; 17 of 171..1203 under a window of 270, 8.9 and
-// 10.6; 8 of 2000, 4 KV heads, where shares of 8 meet the segments' ends, 12.9
-// and 11.0.  2 is slower again: 11.6 against 10.2 for 2 of 3000.
+// 8: one sequence of 1000 / 4000 tokens, 8 KV heads, 9.9 / 10.6 and 11.4 / 10.8
+// us; 32 of 200, 9.3 both; 17 of 171..1203 under a window of 270, 9.4 and 11.2;
+// 8 of 2000, 4 KV heads, where shares of 8 meet the segments' ends, 11.9 and
+// 11.0.  With 2, one of 1000 takes 10.4, the others as much.
 constexpr int kPaMinItems = 4;
 // Where a CTA's share is below this many items, its ends move to the ends of
 // segments of at most kPgWarps items (one a warp): 96 sequences of 57..312
-// tokens, 8 KV heads, 18.9 -> 14.9 us, 3 of 273..502 10.7 -> 8.8.  Larger shares
-// would not feel the merge.  Segments of up to 18: mixed (12.9 -> 11.8 for 96
-// under a window, 9.9 -> 11.1 for one of 1000).
+// tokens, 8 KV heads, 19.8 -> 16.3 us, 3 of 273..502 11.4 -> 9.2, one of 300, 2
+// KV heads, 10.3 -> 8.0.  Larger shares would not feel the merge.  Segments of
+// up to 18 were mixed (faster for 96 under a window, slower for one of 1000).
 constexpr int kPaSnap = 64;
 static_assert(kPaTailBytes <= kPaK && kPaTailBytes <= kPaV, "a tail item fits the buffers");
 static_assert(kPgPart * 4 <= kPaWarpBytes, "a warp's partial fits its buffers");
@@ -309,6 +314,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
     }
   };
   // the lane that holds an item's descriptor requests its copies
+  // Out of L2 first, shared pages too: 64 sequences that share 20000 tokens take
+  // 271.6 us with and without the hint, pages of their own 2 to 4 % less with it.
   const uint64_t pol = policy_evict_first();
   auto issue_k = [&](int x, int st) {
     if (lane == x - base) {
