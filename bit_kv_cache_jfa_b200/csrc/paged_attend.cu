@@ -693,7 +693,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attend_kernel(const __gri
 #pragma unroll
       for (int x = 0; x < 4; ++x) u[x] = visible(t0 + gid + 8 * (x >> 1)) ? d[x] * p.kappa : -INFINITY;
       raise_max(fmaxf(u[0], u[2]), fmaxf(u[1], u[3]));
-      // weights as a bf16 high part and its remainder (16 bits together)
+      // weights as a bf16 high part and its remainder: values are bf16 (fp16 would
+      // not hold them), so the weights are too; 2^-17 of one at most is left out
       uint32_t ph[2], pl[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {

@@ -9,7 +9,9 @@
 // Angles: f_i comes as a 64-bit fraction of a turn, F = f_i / 2 pi * 2^64, so
 // p F mod 2^64 is the angle's fraction of a turn without a range reduction,
 // its error p times F's (2^-53 f_i from the host's 64-bit arithmetic: 1e-9 at
-// a position of ten million); its upper 32 bits go to sincospif.
+// a position of ten million); its upper 32 bits go to sincospif, as the nearest
+// fp32 number of half turns: 2^-25 of one, 1e-7 of a channel, where bf16 outputs
+// keep 2^-9.
 #include "jfa_paged.cuh"
 
 namespace jfa {
